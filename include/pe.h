@@ -480,6 +480,189 @@ pe_status pe_merger_last_error(pe_merger *pm);
 /* pe_merger_destroy -- waits for the device, frees everything; NULL is a no-op. */
 void pe_merger_destroy(pe_merger *pm);
 
+/* ------------------------------------------------------------------------
+ * Operators of the vision tower between the PatchEmbed and the PatchMerger
+ * (mytransformer README §3.2 and §4.1: blocks of LayerNorm, attention with
+ * rotary positions inside each image, MLP): rotary positions, LayerNorm and
+ * attention, each with its gradient.  These calls own no device memory except
+ * the attention handle's error word: buffers and workspaces are the caller's,
+ * so calls with buffers of their own may run at the same time on any streams,
+ * and every call may be captured into a CUDA graph.  Results do not depend on
+ * scheduling: two runs on the same inputs give the same bits.
+ */
+
+/* Largest number of rotated pairs and of position axes pe_rope accepts. */
+#define PE_ROPE_MAX_PAIRS 128
+#define PE_ROPE_MAX_AXES 4
+
+/* A dev tensor [rows, heads, D] with the D elements of a head contiguous; the
+ * strides are in elements.  A tensor with one row or one head may give any
+ * stride for that axis. */
+typedef struct {
+    void *ptr;           /* inputs are only read */
+    int64_t row_stride;
+    int64_t head_stride;
+} pe_heads;
+
+/*
+ * pe_vision_positions -- the (t, h, w) position of every patch row and the
+ * boundaries of the frames, computed on the device from the grids.
+ *   grid_thw : host [n, 3] as in pe_forward_frames_grouped (read before the
+ *              call returns)
+ *   merge    : 1..4, the side of the merge window; gh and gw multiples of it.
+ *              Rows are in the order of the forward calls: m x m windows
+ *              consecutive, row-major inside a frame (mytransformer README
+ *              §3.2 and §4.1).
+ *   pos      : dev int32 [3, N] (t, then h, then w of each row), or NULL
+ *   cu       : dev int32 [F + 1], F = sum_i gt_i frames: cu[f] is the first row
+ *              of frame f and cu[F] = N, or NULL.  The tower's attention stays
+ *              inside a frame, so this is the cu_q of pe_attention_forward.
+ * pos and cu need 4-byte alignment only.  One launch per 64 items.  n = 0 writes
+ * cu[0] = 0.  Errors: PE_ERR_INVALID_ARG, PE_ERR_SHAPE (a size < 1, or not a
+ * multiple of merge), PE_ERR_ALIGN, PE_ERR_UNSUPPORTED (N >= 2^31), PE_ERR_CUDA.
+ */
+pe_status pe_vision_positions(int n, const int32_t *grid_thw, int merge, int32_t *pos, int32_t *cu,
+                              pe_stream_t stream);
+
+/*
+ * pe_rope -- rotary positions with one or several axes, on q and k in one launch.
+ *   q, k     : [N, Hq, D] and [N, Hk, D] of dtype dt; Hk = 0 leaves k and k_out unused
+ *   pos      : dev int32 [axes, N]
+ *   sections : host [axes]: how many pairs of a head each axis turns, in order
+ *              (an entry may be 0).  With S = sum(sections), pair i holds
+ *              elements i and i + S of a head; elements from 2 S on are copied.
+ *   axial    : 0: one ladder of frequencies over all pairs, pair i has rate
+ *              theta^(-i/S) (the language model's M-RoPE, sections 16, 24, 24:
+ *              Qwen2.5VL语言模型).  1: one ladder per axis, pair j of axis a
+ *              has rate theta^(-j/sections[a]) (the vision tower's 2-D rotary
+ *              positions: sections D/4, D/4 and the h and w axes:
+ *              mytransformer README §4.1).
+ *   inverse  : 0 turns by +angle; 1 by -angle, which is the gradient
+ *   q_out, k_out : as q and k; each may be its input itself (same pointer and
+ *              strides), but no other overlap is allowed
+ * angle = pos * rate, reduced in 64 bits; the turn is computed in fp32 and
+ * rounded once.  Pointers need only the alignment of dt.
+ * Requires 1 <= D <= 1024, 1 <= S <= PE_ROPE_MAX_PAIRS, 2 S <= D, 1 <= axes <=
+ * PE_ROPE_MAX_AXES, theta > 0 and finite, N < 2^31, Hq >= 1, strides >= 0.
+ * Errors: PE_ERR_INVALID_ARG, PE_ERR_SHAPE, PE_ERR_DTYPE, PE_ERR_ALIGN,
+ * PE_ERR_UNSUPPORTED, PE_ERR_CUDA.
+ */
+pe_status pe_rope(pe_heads q, pe_heads k, pe_dtype dt, int64_t N, int Hq, int Hk, int D, const int32_t *pos, int axes,
+                  const int32_t *sections, double theta, int axial, int inverse, pe_heads q_out, pe_heads k_out,
+                  pe_stream_t stream);
+
+/* Widest row the layer-norm calls accept. */
+#define PE_LAYERNORM_MAX_E 16384
+
+/*
+ * pe_layernorm_forward -- y = (x - mean) * rstd * gamma + beta over the E
+ * features of each row, rstd = 1 / sqrt(var + eps) with the biased variance (the
+ * PatchMerger's LayerNorm as an operator of its own).
+ *   x, y        : dev [N, E] of dtype dt; y may be x
+ *   gamma, beta : dev [E] of dtype w_dt; NULL stands for ones / zeros
+ *   mean, rstd  : dev fp32 [N] for the backward call, or both NULL
+ * Statistics and arithmetic in fp32 (the variance from the deviations), one
+ * rounding at the end.  E a multiple of 8, at most PE_LAYERNORM_MAX_E; eps >= 0.
+ * Errors: PE_ERR_INVALID_ARG, PE_ERR_DTYPE, PE_ERR_ALIGN, PE_ERR_UNSUPPORTED,
+ * PE_ERR_CUDA.
+ */
+pe_status pe_layernorm_forward(const void *x, pe_dtype dt, int64_t N, int E, const void *gamma, const void *beta,
+                               pe_dtype w_dt, float eps, void *y, float *mean, float *rstd, pe_stream_t stream);
+
+/*
+ * pe_layernorm_backward -- the gradients of pe_layernorm_forward.  With xh =
+ * (x - mean) * rstd and a = dy * gamma:
+ *   dx = rstd * (a - mean_E(a) - xh * mean_E(a * xh)),
+ *   dgamma = sum_n dy * xh,  dbeta = sum_n dy.
+ *   dy, x, dx     : dev [N, E] of dtype dt; dx may be dy or x
+ *   gamma         : dev [E] of dtype w_dt, or NULL for ones
+ *   mean, rstd    : dev fp32 [N], as the forward call wrote them
+ *   dgamma, dbeta : dev [E] of dtype w_dt, overwritten, or both NULL (a frozen
+ *                   weight); N = 0 writes zeros
+ *   ws            : dev, at least pe_layernorm_backward_workspace(N, E) bytes
+ *                   (unused, and may be NULL, when dgamma is NULL)
+ * All sums in fp32 in a fixed order.  Errors: as pe_layernorm_forward;
+ * PE_ERR_SHAPE when the workspace is too small.
+ */
+pe_status pe_layernorm_backward(const void *dy, const void *x, pe_dtype dt, int64_t N, int E, const void *gamma,
+                                pe_dtype w_dt, const float *mean, const float *rstd, void *dx, void *dgamma,
+                                void *dbeta, void *ws, int64_t ws_bytes, pe_stream_t stream);
+
+/* Bytes of workspace pe_layernorm_backward needs; -1 for sizes it refuses. */
+int64_t pe_layernorm_backward_workspace(int64_t N, int E);
+
+/*
+ * Attention over sequences packed one behind the other: the rows of sequence s
+ * attend to the keys of sequence s only (the tower's block-diagonal mask:
+ * mytransformer README §4.1).
+ *     s_ij = scale * q_i . k_j,  lse_i = log sum_j exp(s_ij),
+ *     out_i = sum_j exp(s_ij - lse_i) v_j.
+ * bf16 operands on the tensor cores, fp32 scores, statistics and sums; the
+ * probabilities (and, in the gradient, their derivatives) are rounded to bf16
+ * as operands of the second product.
+ */
+typedef struct pe_attention pe_attention;
+
+/*
+ * pe_attention_create -- Hq query heads on Hkv key/value heads (Hq a multiple of
+ * Hkv; query head h reads key head h / (Hq / Hkv)) of D elements, D a multiple
+ * of 8, 8 <= D <= 128; scale > 0 and finite.  causal = 1: row i of a sequence
+ * of lq queries and lk keys sees keys j <= i + lk - lq (the last row sees all).
+ * Binds to the current CUDA device.  Errors: PE_ERR_INVALID_ARG,
+ * PE_ERR_UNSUPPORTED, PE_ERR_CUDA.
+ */
+pe_status pe_attention_create(int Hq, int Hkv, int D, float scale, int causal, pe_attention **out);
+
+/*
+ * Bytes of workspace a forward call with the same sizes needs, or (backward =
+ * 1) a backward call.  -1 for sizes the calls refuse.
+ */
+int64_t pe_attention_workspace(const pe_attention *a, int n_seq, int64_t Nq, int64_t Nk, int backward);
+
+/*
+ * pe_attention_forward
+ *   cu_q, cu_k : dev int32 [n_seq + 1], non-decreasing, at least 0 and at most
+ *                Nq / Nk: sequence s holds query rows cu_q[s] .. cu_q[s+1] - 1
+ *                and key rows cu_k[s] .. cu_k[s+1] - 1; either may be empty.
+ *                Values outside that contract give unspecified results, but no
+ *                access outside the buffers.  cu_k may be cu_q.
+ *   q, out     : [Nq, Hq, D] bf16;  k, v : [Nk, Hkv, D] bf16
+ *   lse        : dev fp32 [Hq, Nq], natural logarithm, or NULL
+ *   ws         : dev, 16-byte aligned, at least pe_attention_workspace bytes
+ * q, k, v, out must be 16-byte aligned with strides that are multiples of 8
+ * elements and at least D (pe_heads), and smaller than 2^39 elements.  A row
+ * that sees no key gets out = 0 and lse = -inf.  Rows of no sequence are left
+ * as they were.  n_seq = 0 or Nq = 0: nothing is launched.
+ * Errors: PE_ERR_INVALID_ARG, PE_ERR_SHAPE, PE_ERR_ALIGN, PE_ERR_UNSUPPORTED
+ * (Nq or Nk >= 2^31), PE_ERR_CUDA.
+ */
+pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, int64_t Nq, const int32_t *cu_k,
+                               int64_t Nk, pe_heads q, pe_heads k, pe_heads v, pe_heads out, float *lse, void *ws,
+                               int64_t ws_bytes, pe_stream_t stream);
+
+/*
+ * pe_attention_backward -- the gradients of q, k and v for the gradient dout of
+ * out; out and lse are the forward call's.  The probabilities are recomputed:
+ *     delta_i = dout_i . out_i,  p_ij = exp(s_ij - lse_i),
+ *     dv_j = sum_i p_ij dout_i,  ds_ij = p_ij (dout_i . v_j - delta_i),
+ *     dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,
+ * the sums for dk and dv over the query heads that share the key head as well.
+ *   dq : [Nq, Hq, D] bf16;  dk, dv : [Nk, Hkv, D] bf16, layouts as above.  None
+ *   may overlap an input.  Rows that see no key, and keys that no row sees, get
+ *   zero gradients; rows of no sequence are left as they were.
+ * Other arguments and errors as pe_attention_forward (lse not NULL).
+ */
+pe_status pe_attention_backward(pe_attention *a, int n_seq, const int32_t *cu_q, int64_t Nq, const int32_t *cu_k,
+                                int64_t Nk, pe_heads q, pe_heads k, pe_heads v, pe_heads out, const float *lse,
+                                pe_heads dout, pe_heads dq, pe_heads dk, pe_heads dv, void *ws, int64_t ws_bytes,
+                                pe_stream_t stream);
+
+/* pe_attention_last_error -- as pe_last_error, for the attention kernels. */
+pe_status pe_attention_last_error(pe_attention *a);
+
+/* pe_attention_destroy -- waits for the device, frees the handle; NULL is a no-op. */
+void pe_attention_destroy(pe_attention *a);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,5 +1,8 @@
 """B200-native vision PatchEmbed (Qwen2-VL / Qwen2.5-VL) over the libpe.so C ABI.
 
+The operators of the vision tower's blocks (rotary positions, layer norm,
+attention, with their gradients) are in ``tower`` and exported here.
+
 ``PatchEmbed`` is a convenience wrapper holding one ``pe_handle``; every method
 forwards to the same-named C entry point (``_binding``) with torch tensors
 turned into raw device pointers and the current CUDA stream.  PyTorch only
@@ -14,7 +17,8 @@ import torch
 from . import _binding as B
 from ._binding import PE_BF16, PE_F32, PEError, load  # noqa: F401
 
-__all__ = ["PatchEmbed", "PatchMerger", "PEError", "PE_F32", "PE_BF16", "load", "num_patches"]
+__all__ = ["PatchEmbed", "PatchMerger", "PEError", "PE_F32", "PE_BF16", "load", "num_patches",
+           "vision_positions", "rope", "layer_norm", "layer_norm_backward", "Attention"]
 
 
 def _dt(t: torch.dtype) -> int:
@@ -322,3 +326,6 @@ class PatchMerger:
         except Exception:
             pass
 
+
+
+from .tower import Attention, layer_norm, layer_norm_backward, rope, vision_positions  # noqa: E402

@@ -37,7 +37,15 @@ EXPORTS = (
     "pe_merger_create", "pe_merger_set_weights", "pe_merger_forward", "pe_merger_last_error", "pe_merger_destroy",
     "pe_merger_profile_begin", "pe_merger_profile_end", "pe_forward_frames_grouped_host", "pe_forward_patches_host",
     "pe_selftest_wait_timeout", "pe_profile_target",
+    "pe_vision_positions", "pe_rope", "pe_layernorm_forward", "pe_layernorm_backward",
+    "pe_layernorm_backward_workspace", "pe_attention_create", "pe_attention_workspace", "pe_attention_forward",
+    "pe_attention_backward", "pe_attention_last_error", "pe_attention_destroy",
 )
+
+
+class pe_heads(ctypes.Structure):
+    """[rows, heads, D] tensor of include/pe.h: pointer and element strides."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class PEError(RuntimeError):
@@ -62,6 +70,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib = ctypes.CDLL(p)
     vp, i32, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
     i32p = ctypes.POINTER(ctypes.c_int32)
+    hd, f32 = pe_heads, ctypes.c_float
     f32p = ctypes.POINTER(ctypes.c_float)
     sig = {
         "pe_create": ([i32, i32, i32, i32, i32, ctypes.POINTER(vp)], i32),
@@ -97,6 +106,17 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "pe_profile_target": ([vp, i32], i32),
         "pe_profile_end": ([vp, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(i32),
                             ctypes.POINTER(ctypes.c_int64)], i32),
+        "pe_vision_positions": ([i32, i32p, i32, vp, vp, vp], i32),
+        "pe_rope": ([hd, hd, i32, i64, i32, i32, i32, vp, i32, i32p, ctypes.c_double, i32, i32, hd, hd, vp], i32),
+        "pe_layernorm_forward": ([vp, i32, i64, i32, vp, vp, i32, f32, vp, vp, vp, vp], i32),
+        "pe_layernorm_backward": ([vp, vp, i32, i64, i32, vp, i32, vp, vp, vp, vp, vp, vp, i64, vp], i32),
+        "pe_layernorm_backward_workspace": ([i64, i32], i64),
+        "pe_attention_create": ([i32, i32, i32, f32, i32, ctypes.POINTER(vp)], i32),
+        "pe_attention_workspace": ([vp, i32, i64, i64, i32], i64),
+        "pe_attention_forward": ([vp, i32, vp, i64, vp, i64, hd, hd, hd, hd, vp, vp, i64, vp], i32),
+        "pe_attention_backward": ([vp, i32, vp, i64, vp, i64, hd, hd, hd, hd, vp, hd, hd, hd, hd, vp, i64, vp], i32),
+        "pe_attention_last_error": ([vp], i32),
+        "pe_attention_destroy": ([vp], None),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -308,3 +328,65 @@ def pe_selftest_wait_timeout(h: int, stream: int) -> None:
 
 def pe_last_error(h: int) -> int:
     return int(load().pe_last_error(h))
+
+
+def pe_vision_positions(grid_thw: Sequence[Sequence[int]], merge: int, pos_ptr: Optional[int], cu_ptr: Optional[int],
+                        stream: int) -> None:
+    n = len(grid_thw)
+    _check("pe_vision_positions", load().pe_vision_positions(n, _i32rows(grid_thw) if n else None, merge, pos_ptr,
+                                                             cu_ptr, stream))
+
+
+def pe_rope(q: pe_heads, k: pe_heads, dt: int, N: int, Hq: int, Hk: int, D: int, pos_ptr: int, sections: Sequence[int],
+            theta: float, axial: bool, inverse: bool, q_out: pe_heads, k_out: pe_heads, stream: int) -> None:
+    _check("pe_rope", load().pe_rope(q, k, dt, N, Hq, Hk, D, pos_ptr, len(sections), _i32arr(sections), theta,
+                                     int(bool(axial)), int(bool(inverse)), q_out, k_out, stream))
+
+
+def pe_layernorm_forward(x_ptr: int, dt: int, N: int, E: int, gamma: Optional[int], beta: Optional[int], w_dt: int,
+                         eps: float, y_ptr: int, mean: Optional[int], rstd: Optional[int], stream: int) -> None:
+    _check("pe_layernorm_forward", load().pe_layernorm_forward(x_ptr, dt, N, E, gamma, beta, w_dt, eps, y_ptr, mean,
+                                                               rstd, stream))
+
+
+def pe_layernorm_backward(dy_ptr: int, x_ptr: int, dt: int, N: int, E: int, gamma: Optional[int], w_dt: int, mean: int,
+                          rstd: int, dx_ptr: int, dgamma: Optional[int], dbeta: Optional[int], ws: Optional[int],
+                          ws_bytes: int, stream: int) -> None:
+    _check("pe_layernorm_backward", load().pe_layernorm_backward(dy_ptr, x_ptr, dt, N, E, gamma, w_dt, mean, rstd,
+                                                                 dx_ptr, dgamma, dbeta, ws, ws_bytes, stream))
+
+
+def pe_layernorm_backward_workspace(N: int, E: int) -> int:
+    return int(load().pe_layernorm_backward_workspace(N, E))
+
+
+def pe_attention_create(Hq: int, Hkv: int, D: int, scale: float, causal: bool) -> int:
+    h = ctypes.c_void_p()
+    _check("pe_attention_create", load().pe_attention_create(Hq, Hkv, D, scale, int(bool(causal)), ctypes.byref(h)))
+    return h.value
+
+
+def pe_attention_workspace(a: int, n_seq: int, Nq: int, Nk: int, backward: bool) -> int:
+    return int(load().pe_attention_workspace(a, n_seq, Nq, Nk, int(bool(backward))))
+
+
+def pe_attention_forward(a: int, n_seq: int, cu_q: int, Nq: int, cu_k: int, Nk: int, q: pe_heads, k: pe_heads,
+                         v: pe_heads, out: pe_heads, lse: Optional[int], ws: Optional[int], ws_bytes: int,
+                         stream: int) -> None:
+    _check("pe_attention_forward", load().pe_attention_forward(a, n_seq, cu_q, Nq, cu_k, Nk, q, k, v, out, lse, ws,
+                                                               ws_bytes, stream))
+
+
+def pe_attention_backward(a: int, n_seq: int, cu_q: int, Nq: int, cu_k: int, Nk: int, q: pe_heads, k: pe_heads,
+                          v: pe_heads, out: pe_heads, lse: int, dout: pe_heads, dq: pe_heads, dk: pe_heads,
+                          dv: pe_heads, ws: Optional[int], ws_bytes: int, stream: int) -> None:
+    _check("pe_attention_backward", load().pe_attention_backward(a, n_seq, cu_q, Nq, cu_k, Nk, q, k, v, out, lse, dout,
+                                                                 dq, dk, dv, ws, ws_bytes, stream))
+
+
+def pe_attention_last_error(a: int) -> int:
+    return int(load().pe_attention_last_error(a))
+
+
+def pe_attention_destroy(a: int) -> None:
+    load().pe_attention_destroy(a)

@@ -5,7 +5,6 @@
 // pe_kernels.cuh.
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
 #include <cmath>
@@ -18,6 +17,7 @@
 
 #include "../../include/pe.h"
 #include "pe_host_plan.h"
+#include "pe_host_util.h"
 #include "pe_kernels.cuh"
 #include "pe_astat.cuh"
 
@@ -81,23 +81,6 @@ struct pe_handle {
 
 namespace {
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    if (!fn) {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    }
-    return fn;
-}
-
 // 2-D tensor [rows, cols] (cols contiguous, row stride `ld` elements) of bf16 or
 // fp32, box [box_rows, box_cols]; out-of-bounds elements read as zero and are
 // not written by stores.
@@ -125,46 +108,6 @@ bool make_out_tmap(CUtensorMap *m, void *out, bool f32, int64_t N, int E) {
     return make_tmap(m, out, f32, (uint64_t)N, (uint64_t)E, (uint64_t)E, 32, 32,
                      f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
-
-// One NVTX range per public call, named after it: visible on Nsight timelines
-// and usable as an ncu filter (--nvtx --nvtx-include); without a tool attached
-// the push and pop return at once.
-struct NvtxRange {
-    explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-    NvtxRange(const NvtxRange &) = delete;
-    NvtxRange &operator=(const NvtxRange &) = delete;
-};
-
-// Runs an entry point's body so that no C++ exception crosses the C ABI: a
-// failed host allocation (the item tables and chunk plans are std::vectors)
-// returns PE_ERR_HOST_MEMORY, anything else PE_ERR_CUDA.
-template <class F>
-pe_status no_throw(F &&body) {
-    try {
-        return body();
-    } catch (const std::bad_alloc &) {
-        return PE_ERR_HOST_MEMORY;
-    } catch (...) {
-        return PE_ERR_CUDA;
-    }
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool valid_dtype(int d) { return d == PE_F32 || d == PE_BF16; }
-
-struct DeviceGuard {
-    int prev = -1;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-        if (prev != dev) cudaSetDevice(dev);
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
 
 int bn_override() {
     const char *s = std::getenv("PE_BN");
@@ -359,8 +302,6 @@ size_t plan_pipeline(const pe_handle *h, FwdParams &P, int amode, int kcols = -1
     P.epi_offset = (int)((rings(nb, na) + 1023) / 1024 * 1024);
     return total(nb, na);
 }
-
-pe_status finish(cudaError_t e) { return e == cudaSuccess ? PE_OK : PE_ERR_CUDA; }
 
 // Validate one frames item and fill its descriptor.  Returns PE_OK or an error.
 pe_status make_item(const pe_handle *h, const void *frames, int T, int H, int W, const int32_t *g,

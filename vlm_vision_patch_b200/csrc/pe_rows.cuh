@@ -1,0 +1,369 @@
+// Row-wise kernels of the vision tower: patch positions from grids, rotary
+// positions, and layer norm with its gradient.  All are bound by HBM (or, on one
+// image, by launch latency): each reads its rows once with 16-byte loads, keeps
+// them in registers and writes once.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "pe_device.cuh"
+
+namespace pe {
+
+// ------------------------------------------------------------- positions
+
+constexpr int kGridItems = 64;   // items per launch, carried in the launch parameters
+
+struct GridItem {
+    int row0, frame0, h, w;      // first row and frame of the item, frame size in patches
+};
+struct GridChunk {
+    GridItem item[kGridItems];
+    int n, row_end, frame_end;   // items; rows and frames before the chunk's end
+    int last;                    // the last chunk also writes cu[F] = N
+};
+
+// Largest i with item[i].row0 <= r (items hold at least one row and frame each).
+template <class Key>
+__device__ __forceinline__ int find_item(const GridChunk &c, int r, Key key) {
+    int lo = 0, hi = c.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (key(c.item[mid]) <= r) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// One thread per row (and per frame boundary).  Row r of a frame: window r / m^2,
+// place r % m^2 inside it, both row-major.
+__global__ void pe_positions_kernel(const __grid_constant__ GridChunk c, int m, int64_t N, int32_t *pos, int32_t *cu) {
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (c.n == 0) {
+        if (i == 0 && cu) cu[0] = 0;
+        return;
+    }
+    const int64_t r = c.item[0].row0 + i;
+    if (pos && r < c.row_end) {
+        const GridItem g = c.item[find_item(c, (int)r, [](const GridItem &t) { return t.row0; })];
+        const unsigned area = (unsigned)g.h * (unsigned)g.w, in_item = (unsigned)((int)r - g.row0);
+        const unsigned f = in_item / area, in_frame = in_item - f * area;
+        const unsigned m2 = (unsigned)(m * m), win = in_frame / m2, at = in_frame - win * m2;
+        const unsigned across = (unsigned)(g.w / m), wr = win / across, wc = win - wr * across;
+        const unsigned ar = at / (unsigned)m, ac = at - ar * (unsigned)m;
+        pos[r] = (int32_t)f;
+        pos[N + r] = (int32_t)(wr * (unsigned)m + ar);
+        pos[2 * N + r] = (int32_t)(wc * (unsigned)m + ac);
+    }
+    const int64_t f = c.item[0].frame0 + i;
+    if (cu && f < c.frame_end) {
+        const GridItem g = c.item[find_item(c, (int)f, [](const GridItem &t) { return t.frame0; })];
+        cu[f] = g.row0 + ((int)f - g.frame0) * (g.h * g.w);
+    }
+    if (cu && c.last && i == 0) cu[c.frame_end] = (int32_t)N;
+}
+
+// ------------------------------------------------------------- elements
+
+// 8 consecutive elements as fp32.
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = bf16lo_to_f32(w[i]), v[2 * i + 1] = bf16hi_to_f32(w[i]);
+}
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+// 8 elements of a weight of either type, or `fill` without one.
+__device__ __forceinline__ void load8_weight(const void *w, bool f32, int64_t e, float fill, float (&v)[8]) {
+    if (!w) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = fill;
+    } else if (f32) {
+        load8(static_cast<const float *>(w) + e, v);
+    } else {
+        load8(static_cast<const __nv_bfloat16 *>(w) + e, v);
+    }
+}
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <class T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// ------------------------------------------------------------- rotary positions
+
+struct RopeSide {
+    const void *in;
+    void *out;
+    int64_t in_row, in_head, out_row, out_head;   // strides in elements
+    int heads;
+};
+struct RopeParams {
+    RopeSide s[2];               // q, k
+    const int32_t *pos;          // [axes, N]
+    int64_t N;
+    int pairs, tail, rows;       // S, D - 2 S, rows per block
+    float sign;
+    uint8_t axis[128];           // of pair i
+    double turns[128];           // rate of pair i in turns: rate / (2 pi)
+};
+
+template <class T, int VEC>
+struct alignas(sizeof(T) * VEC) Pack {
+    T v[VEC];
+};
+
+// A block turns `rows` rows.  Their cosines and sines are computed once into
+// shared memory (all heads of q and k share them): the angle in turns is a
+// 64-bit product reduced to [-1/2, 1/2] exactly, so a position of a million
+// costs no accuracy, and 64 bits are spent on S values a row, not on every
+// element.  Then each thread turns VEC pairs at a time.
+template <class T, int VEC>
+__global__ void __launch_bounds__(256) pe_rope_kernel(const __grid_constant__ RopeParams P) {
+    extern __shared__ float2 cs[];                       // [rows][pairs] (cos, sin)
+    const int S = P.pairs;
+    const int64_t row0 = (int64_t)blockIdx.x * P.rows;
+    const int rows = (int)(P.N - row0 < P.rows ? P.N - row0 : P.rows);
+    for (int i = threadIdx.x; i < rows * S; i += blockDim.x) {
+        const int r = i / S, p = i - r * S;
+        const double t = (double)P.pos[(int64_t)P.axis[p] * P.N + row0 + r] * P.turns[p];
+        const float u = (float)(t - rint(t));
+        float s, c;
+        sincospif(2.0f * u, &s, &c);
+        cs[i] = make_float2(c, P.sign * s);
+    }
+    __syncthreads();
+    const int sv = S / VEC, tv = P.tail / VEC, per_head = sv + tv;
+    const int heads = P.s[0].heads + P.s[1].heads, per_row = heads * per_head;
+    for (int i = threadIdx.x; i < rows * per_row; i += blockDim.x) {
+        const int r = i / per_row, j = i - r * per_row;
+        int h = j / per_head;
+        const int v = j - h * per_head;
+        const bool second = h >= P.s[0].heads;
+        const RopeSide &s = P.s[second];
+        if (second) h -= P.s[0].heads;
+        const T *in = static_cast<const T *>(s.in) + (row0 + r) * s.in_row + h * s.in_head;
+        T *out = static_cast<T *>(s.out) + (row0 + r) * s.out_row + h * s.out_head;
+        using V = Pack<T, VEC>;
+        if (v < sv) {
+            const V a = *reinterpret_cast<const V *>(in + v * VEC), b = *reinterpret_cast<const V *>(in + S + v * VEC);
+            V x, y;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float2 t = cs[r * S + v * VEC + e];
+                const float f = to_f32(a.v[e]), g = to_f32(b.v[e]);
+                // the roundings are written out, so that every VEC gives the same bits
+                x.v[e] = from_f32<T>(__fmaf_rn(f, t.x, -__fmul_rn(g, t.y)));
+                y.v[e] = from_f32<T>(__fmaf_rn(g, t.x, __fmul_rn(f, t.y)));
+            }
+            *reinterpret_cast<V *>(out + v * VEC) = x;
+            *reinterpret_cast<V *>(out + S + v * VEC) = y;
+        } else if (in != out) {
+            const int e = 2 * S + (v - sv) * VEC;
+            *reinterpret_cast<V *>(out + e) = *reinterpret_cast<const V *>(in + e);
+        }
+    }
+}
+
+// ------------------------------------------------------------- layer norm
+//
+// TPR threads hold one row in registers, VPT groups of 8 elements each, so x is
+// read once and the variance is taken from the deviations.  A warp per row up
+// to 1280 features, 128 threads up to 4096, 512 beyond (VPT <= 5 keeps the
+// backward kernel's 16 sums per group in registers).
+
+// Sum of v over the TPR threads of a row (all of them get it); blocks hold
+// blockDim / TPR rows.  `red`: TPR / 32 floats per row.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float *red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if constexpr (TPR > 32) {
+        __syncthreads();                                  // the last sum has been read
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+        __syncthreads();
+        const int base = threadIdx.x / TPR * (TPR / 32);
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < TPR / 32; ++i) v += red[base + i];
+    }
+    return v;
+}
+
+struct NormParams {
+    const void *x, *dy, *gamma, *beta;
+    void *y;                      // forward: y; backward: dx
+    float *mean, *rstd;
+    float *part;                  // backward: [gridDim][2][E] partial sums, or NULL
+    int64_t N;
+    int E, w_f32;
+    float eps;
+};
+
+template <int TPR>
+constexpr int kNormThreads = TPR == 512 ? 512 : 128;
+
+template <class T, int TPR, int VPT>
+__global__ void __launch_bounds__(kNormThreads<TPR>) pe_norm_fwd_kernel(const NormParams P) {
+    __shared__ float red[kNormThreads<TPR> / 32];
+    constexpr int kRows = kNormThreads<TPR> / TPR;
+    const int t = threadIdx.x % TPR, nv = P.E / 8;
+    const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+    if (TPR == 32 && row >= P.N) return;                  // wider rows: one per block
+    const T *x = static_cast<const T *>(P.x) + row * P.E;
+    float v[VPT][8];
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        if (t + i * TPR < nv) {
+            load8(x + 8 * (t + i * TPR), v[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += v[i][e];
+        }
+    }
+    const float mean = row_sum<TPR>(s, red) / (float)P.E;
+    float q = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+        if (t + i * TPR < nv)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q += (v[i][e] - mean) * (v[i][e] - mean);
+    const float rstd = 1.0f / sqrtf(row_sum<TPR>(q, red) / (float)P.E + P.eps);
+    T *y = static_cast<T *>(P.y) + row * P.E;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        if (t + i * TPR < nv) {
+            const int e0 = 8 * (t + i * TPR);
+            float g[8], b[8];
+            load8_weight(P.gamma, P.w_f32, e0, 1.f, g);
+            load8_weight(P.beta, P.w_f32, e0, 0.f, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[i][e] = (v[i][e] - mean) * rstd * g[e] + b[e];
+            store8(y + e0, v[i]);
+        }
+    }
+    if (P.mean && t == 0) {
+        P.mean[row] = mean;
+        P.rstd[row] = rstd;
+    }
+}
+
+// Each block takes rows blockIdx, blockIdx + gridDim, ... (in groups of its rows
+// at once), writes dx, and keeps the sums over its rows of dy * xh and dy for
+// its features in registers; they go to part[blockIdx] once.  No atomics: the
+// order of every sum is fixed by the sizes.
+template <class T, int TPR, int VPT>
+__global__ void __launch_bounds__(kNormThreads<TPR>) pe_norm_bwd_kernel(const NormParams P) {
+    extern __shared__ float sums[];                       // [rows per block - 1][2][E] when part
+    __shared__ float red[kNormThreads<TPR> / 32];
+    constexpr int kRows = kNormThreads<TPR> / TPR;
+    const int t = threadIdx.x % TPR, lane_row = threadIdx.x / TPR, nv = P.E / 8;
+    const float inv_e = 1.0f / (float)P.E;
+    float dg[VPT][8], db[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dg[i][e] = db[i][e] = 0.f;
+    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < P.N; r0 += (int64_t)gridDim.x * kRows) {
+        const int64_t row = r0 + lane_row;
+        if (TPR == 32 && row >= P.N) break;               // whole warps; wider rows: one per block
+        const T *x = static_cast<const T *>(P.x) + row * P.E, *dy = static_cast<const T *>(P.dy) + row * P.E;
+        const float mean = P.mean[row], rstd = P.rstd[row];
+        float xh[VPT][8], a[VPT][8];
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if (t + i * TPR < nv) {
+                const int e0 = 8 * (t + i * TPR);
+                load8(x + e0, xh[i]);
+                load8(dy + e0, a[i]);
+                float g[8];
+                load8_weight(P.gamma, P.w_f32, e0, 1.f, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    xh[i][e] = (xh[i][e] - mean) * rstd;
+                    dg[i][e] += a[i][e] * xh[i][e];
+                    db[i][e] += a[i][e];
+                    a[i][e] *= g[e];
+                    s1 += a[i][e];
+                    s2 += a[i][e] * xh[i][e];
+                }
+            }
+        }
+        s1 = row_sum<TPR>(s1, red) * inv_e;
+        s2 = row_sum<TPR>(s2, red) * inv_e;
+        T *dx = static_cast<T *>(P.y) + row * P.E;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if (t + i * TPR < nv) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) a[i][e] = rstd * (a[i][e] - s1 - xh[i][e] * s2);
+                store8(dx + 8 * (t + i * TPR), a[i]);
+            }
+        }
+    }
+    if (!P.part) return;
+    float *out = P.part + (int64_t)blockIdx.x * 2 * P.E;
+    if constexpr (kRows > 1) {                            // the block's rows, added in order by the first
+        if (lane_row > 0) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                if (t + i * TPR < nv) {
+                    store8(sums + (lane_row - 1) * 2 * P.E + 8 * (t + i * TPR), dg[i]);
+                    store8(sums + (lane_row - 1) * 2 * P.E + P.E + 8 * (t + i * TPR), db[i]);
+                }
+        }
+        __syncthreads();
+        if (lane_row > 0) return;
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        if (t + i * TPR < nv) {
+            const int e0 = 8 * (t + i * TPR);
+            for (int r = 0; r < kRows - 1; ++r) {
+                float u[8], w[8];
+                load8(sums + r * 2 * P.E + e0, u);
+                load8(sums + r * 2 * P.E + P.E + e0, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) dg[i][e] += u[e], db[i][e] += w[e];
+            }
+            store8(out + e0, dg[i]);
+            store8(out + P.E + e0, db[i]);
+        }
+    }
+}
+
+// dgamma and dbeta from `n` partial rows of 2 E: a block sums 32 columns, its 8
+// warps every 8th row, then the 8 sums in order.
+__global__ void __launch_bounds__(256) pe_norm_sum_kernel(const float *part, int n, int E, int w_f32, void *dgamma,
+                                                          void *dbeta) {
+    __shared__ float s[8][33];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + lane;
+    float a = 0.f;
+    if (col < 2 * E)
+        for (int r = w; r < n; r += 8) a += part[(int64_t)r * 2 * E + col];
+    s[w][lane] = a;
+    __syncthreads();
+    if (w != 0 || col >= 2 * E) return;
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += s[i][lane];
+    void *dst = col < E ? dgamma : dbeta;
+    const int e = col < E ? col : col - E;
+    if (w_f32) static_cast<float *>(dst)[e] = v;
+    else static_cast<__nv_bfloat16 *>(dst)[e] = __float2bfloat16_rn(v);
+}
+
+}  // namespace pe

@@ -1,0 +1,460 @@
+// C ABI of the vision-tower operators (see include/pe.h for the contract of
+// every entry point): rotary positions, layer norm and attention.  Host side:
+// argument validation, variant choice and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "../../include/pe.h"
+#include "pe_attention.cuh"
+#include "pe_host_util.h"
+#include "pe_rows.cuh"
+
+using namespace pe;
+
+struct pe_attention {
+    int dev = -1;
+    int Hq = 0, Hkv = 0, D = 0, causal = 0;
+    float scale = 0.f;
+    int num_sms = 0;
+    int *err = nullptr;          // dev error word
+};
+
+namespace {
+
+bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+size_t size_of(pe_dtype dt) { return dt == PE_F32 ? 4 : 2; }
+
+// Streaming multiprocessors of the current device.
+int current_sms() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return n;
+}
+
+// ------------------------------------------------------------- rotary positions
+
+// The widest access (at most 16 bytes) that divides the head's halves and tail,
+// every stride in use and every base address.
+int rope_vec(const RopeParams &P, size_t es) {
+    int vec = (int)(16 / es);
+    auto fits = [&](int v) {
+        if (P.pairs % v || P.tail % v) return false;
+        for (const RopeSide &s : P.s) {
+            if (s.heads == 0) continue;
+            if (!aligned_to(s.in, es * v) || !aligned_to(s.out, es * v)) return false;
+            if (P.N > 1 && (s.in_row % v || s.out_row % v)) return false;
+            if (s.heads > 1 && (s.in_head % v || s.out_head % v)) return false;
+        }
+        return true;
+    };
+    while (vec > 1 && !fits(vec)) vec /= 2;
+    return vec;
+}
+
+template <class T, int VEC>
+cudaError_t launch_rope(const RopeParams &P, cudaStream_t st) {
+    const int64_t blocks = (P.N + P.rows - 1) / P.rows;
+    pe_rope_kernel<T, VEC><<<(unsigned)blocks, 256, (size_t)P.rows * P.pairs * sizeof(float2), st>>>(P);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------- layer norm
+
+// Threads per row (see pe_rows.cuh).
+int norm_tpr(int E) { return E <= 1280 ? 32 : (E <= 4096 ? 128 : 512); }
+
+// Blocks of the backward kernel: each writes one partial row of 2 E sums, so
+// there are no more than fill the GPU.
+int norm_bwd_blocks(int64_t N, int E, int sms) {
+    const int tpr = norm_tpr(E), rows = tpr == 32 ? 4 : 1;
+    return (int)std::min<int64_t>((N + rows - 1) / rows, (int64_t)sms * (tpr == 512 ? 1 : 3));
+}
+
+template <class T, int TPR, int VPT>
+cudaError_t launch_norm(const NormParams &P, bool backward, int blocks, cudaStream_t st) {
+    constexpr int kThreads = kNormThreads<TPR>;
+    if (!backward) {
+        pe_norm_fwd_kernel<T, TPR, VPT><<<(unsigned)blocks, kThreads, 0, st>>>(P);
+    } else {
+        const size_t smem = P.part ? (size_t)(kThreads / TPR - 1) * 2 * P.E * sizeof(float) : 0;
+        pe_norm_bwd_kernel<T, TPR, VPT><<<(unsigned)blocks, kThreads, smem, st>>>(P);
+    }
+    return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t dispatch_norm(const NormParams &P, bool backward, int blocks, cudaStream_t st) {
+    const int tpr = norm_tpr(P.E), vpt = (P.E / 8 + tpr - 1) / tpr;
+    if (tpr == 32) {
+        switch (vpt) {
+            case 1: return launch_norm<T, 32, 1>(P, backward, blocks, st);
+            case 2: return launch_norm<T, 32, 2>(P, backward, blocks, st);
+            case 3: return launch_norm<T, 32, 3>(P, backward, blocks, st);
+            case 4: return launch_norm<T, 32, 4>(P, backward, blocks, st);
+            default: return launch_norm<T, 32, 5>(P, backward, blocks, st);
+        }
+    }
+    if (tpr == 128) {
+        switch (vpt) {
+            case 2: return launch_norm<T, 128, 2>(P, backward, blocks, st);
+            case 3: return launch_norm<T, 128, 3>(P, backward, blocks, st);
+            default: return launch_norm<T, 128, 4>(P, backward, blocks, st);
+        }
+    }
+    switch (vpt) {
+        case 2: return launch_norm<T, 512, 2>(P, backward, blocks, st);
+        case 3: return launch_norm<T, 512, 3>(P, backward, blocks, st);
+        default: return launch_norm<T, 512, 4>(P, backward, blocks, st);
+    }
+}
+
+pe_status check_norm(pe_dtype dt, pe_dtype w_dt, int64_t N, int E) {
+    if (N < 0 || E < 1) return PE_ERR_INVALID_ARG;
+    if (!valid_dtype(dt) || !valid_dtype(w_dt)) return PE_ERR_DTYPE;
+    if (E % 8 || E > PE_LAYERNORM_MAX_E || N > INT32_MAX) return PE_ERR_UNSUPPORTED;
+    return PE_OK;
+}
+
+// ------------------------------------------------------------- attention
+
+// One [rows, heads, D] tensor: present, aligned, with strides a tensor map takes.
+pe_status check_heads(const pe_heads &t, int64_t rows, int heads, int D) {
+    if (!t.ptr) return PE_ERR_INVALID_ARG;
+    if (!aligned16(t.ptr)) return PE_ERR_ALIGN;
+    for (int a = 0; a < 2; ++a) {
+        const int64_t n = a ? heads : rows, st = a ? t.head_stride : t.row_stride;
+        if (n <= 1) continue;
+        if (st < D || st >= ((int64_t)1 << 39)) return PE_ERR_SHAPE;
+        if (st % 8) return PE_ERR_ALIGN;
+    }
+    return PE_OK;
+}
+
+HeadsPtr heads_ptr(const pe_heads &t, int64_t rows, int heads) {
+    return {static_cast<__nv_bfloat16 *>(t.ptr), rows > 1 ? t.row_stride : 0, heads > 1 ? t.head_stride : 0};
+}
+
+// Sizes that do not depend on the buffers.
+pe_status check_attention(const pe_attention *a, int n_seq, int64_t Nq, int64_t Nk) {
+    if (!a || n_seq < 0 || Nq < 0 || Nk < 0) return PE_ERR_INVALID_ARG;
+    if (Nq > INT32_MAX - 256 || Nk > INT32_MAX - 256 || n_seq > (1 << 24)) return PE_ERR_UNSUPPORTED;
+    return PE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pe_status pe_vision_positions(int n, const int32_t *grid, int merge, int32_t *pos, int32_t *cu, pe_stream_t stream) {
+    NvtxRange nvtx("pe_vision_positions");
+    if (n < 0 || (n > 0 && !grid) || merge < 1 || merge > 4) return PE_ERR_INVALID_ARG;
+    if (!aligned_to(pos, 4) || !aligned_to(cu, 4)) return PE_ERR_ALIGN;
+    int64_t N = 0, F = 0;
+    for (int i = 0; i < n; ++i) {
+        const int32_t *g = grid + 3 * (int64_t)i;
+        if (g[0] < 1 || g[1] < 1 || g[2] < 1 || g[1] % merge || g[2] % merge) return PE_ERR_SHAPE;
+        const int64_t area = (int64_t)g[1] * g[2];
+        if (area > INT32_MAX || area * g[0] > INT32_MAX - N) return PE_ERR_UNSUPPORTED;
+        N += area * g[0];
+        F += g[0];
+    }
+    cudaStream_t st = (cudaStream_t)stream;
+    if (!pos && !cu) return PE_OK;
+    int64_t row = 0, frame = 0;
+    int i = 0;
+    do {
+        GridChunk c;
+        std::memset(&c, 0, sizeof(c));
+        const int64_t row0 = row, frame0 = frame;
+        for (; c.n < kGridItems && i < n; ++i, ++c.n) {
+            const int32_t *g = grid + 3 * (int64_t)i;
+            c.item[c.n] = {(int)row, (int)frame, g[1], g[2]};
+            row += (int64_t)g[0] * g[1] * g[2];
+            frame += g[0];
+        }
+        c.row_end = (int)row;
+        c.frame_end = (int)frame;
+        c.last = i == n;
+        const int64_t threads = std::max<int64_t>(pos ? row - row0 : frame - frame0, 1);
+        pe_positions_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(c, merge, N, pos, cu);
+        if (cudaGetLastError() != cudaSuccess) return PE_ERR_CUDA;
+    } while (i < n);
+    return PE_OK;
+}
+
+pe_status pe_rope(pe_heads q, pe_heads k, pe_dtype dt, int64_t N, int Hq, int Hk, int D, const int32_t *pos, int axes,
+                  const int32_t *sections, double theta, int axial, int inverse, pe_heads q_out, pe_heads k_out,
+                  pe_stream_t stream) {
+    NvtxRange nvtx("pe_rope");
+    if (N < 0 || Hq < 1 || Hk < 0 || D < 1 || axes < 1 || !sections || (axial != 0 && axial != 1) ||
+        (inverse != 0 && inverse != 1) || !(theta > 0.0) || !std::isfinite(theta))
+        return PE_ERR_INVALID_ARG;
+    if (!valid_dtype(dt)) return PE_ERR_DTYPE;
+    if (axes > PE_ROPE_MAX_AXES || D > 1024 || N > INT32_MAX) return PE_ERR_UNSUPPORTED;
+    int64_t S = 0;
+    for (int a = 0; a < axes; ++a) {
+        if (sections[a] < 0) return PE_ERR_INVALID_ARG;
+        S += sections[a];
+    }
+    if (S < 1 || 2 * S > D) return PE_ERR_SHAPE;
+    if (S > PE_ROPE_MAX_PAIRS || (int64_t)Hq + Hk > 65536) return PE_ERR_UNSUPPORTED;
+    if (N == 0) return PE_OK;
+    if (!pos) return PE_ERR_INVALID_ARG;
+    if (!aligned_to(pos, 4)) return PE_ERR_ALIGN;
+    const size_t es = size_of(dt);
+    RopeParams P;
+    std::memset(&P, 0, sizeof(P));
+    const pe_heads *in[2] = {&q, &k}, *out[2] = {&q_out, &k_out};
+    for (int i = 0; i < 2; ++i) {
+        const int heads = i ? Hk : Hq;
+        if (heads == 0) continue;
+        if (!in[i]->ptr || !out[i]->ptr) return PE_ERR_INVALID_ARG;
+        if (!aligned_to(in[i]->ptr, es) || !aligned_to(out[i]->ptr, es)) return PE_ERR_ALIGN;
+        if (in[i]->row_stride < 0 || in[i]->head_stride < 0 || out[i]->row_stride < 0 || out[i]->head_stride < 0)
+            return PE_ERR_INVALID_ARG;
+        P.s[i] = {in[i]->ptr, out[i]->ptr, in[i]->row_stride, in[i]->head_stride, out[i]->row_stride,
+                  out[i]->head_stride, heads};
+    }
+    P.pos = pos;
+    P.N = N;
+    P.pairs = (int)S;
+    P.tail = (int)(D - 2 * S);
+    P.sign = inverse ? -1.f : 1.f;
+    const double two_pi = 6.283185307179586476925286766559;
+    for (int a = 0, i = 0; a < axes; ++a)
+        for (int j = 0; j < sections[a]; ++j, ++i) {
+            P.axis[i] = (uint8_t)a;
+            P.turns[i] = std::pow(theta, axial ? -(double)j / sections[a] : -(double)i / (double)S) / two_pi;
+        }
+    P.rows = 8;
+    cudaStream_t st = (cudaStream_t)stream;
+    const int vec = rope_vec(P, es);
+    if (dt == PE_F32) {
+        if (vec == 4) return finish(launch_rope<float, 4>(P, st));
+        return finish(vec == 2 ? launch_rope<float, 2>(P, st) : launch_rope<float, 1>(P, st));
+    }
+    using bf16 = __nv_bfloat16;
+    if (vec == 8) return finish(launch_rope<bf16, 8>(P, st));
+    if (vec == 4) return finish(launch_rope<bf16, 4>(P, st));
+    return finish(vec == 2 ? launch_rope<bf16, 2>(P, st) : launch_rope<bf16, 1>(P, st));
+}
+
+pe_status pe_layernorm_forward(const void *x, pe_dtype dt, int64_t N, int E, const void *gamma, const void *beta,
+                               pe_dtype w_dt, float eps, void *y, float *mean, float *rstd, pe_stream_t stream) {
+    NvtxRange nvtx("pe_layernorm_forward");
+    if (!(eps >= 0.f) || !std::isfinite(eps) || (mean == nullptr) != (rstd == nullptr)) return PE_ERR_INVALID_ARG;
+    if (pe_status s = check_norm(dt, w_dt, N, E); s != PE_OK) return s;
+    if (N == 0) return PE_OK;
+    if (!x || !y) return PE_ERR_INVALID_ARG;
+    for (const void *p : {x, (const void *)y, gamma, beta})
+        if (!aligned16(p)) return PE_ERR_ALIGN;
+    if (!aligned_to(mean, 4) || !aligned_to(rstd, 4)) return PE_ERR_ALIGN;
+    NormParams P;
+    std::memset(&P, 0, sizeof(P));
+    P.x = x;
+    P.gamma = gamma;
+    P.beta = beta;
+    P.y = y;
+    P.mean = mean;
+    P.rstd = rstd;
+    P.N = N;
+    P.E = E;
+    P.w_f32 = w_dt == PE_F32;
+    P.eps = eps;
+    const int rows = norm_tpr(E) == 32 ? 4 : 1, blocks = (int)((N + rows - 1) / rows);
+    cudaStream_t st = (cudaStream_t)stream;
+    return finish(dt == PE_F32 ? dispatch_norm<float>(P, false, blocks, st)
+                               : dispatch_norm<__nv_bfloat16>(P, false, blocks, st));
+}
+
+int64_t pe_layernorm_backward_workspace(int64_t N, int E) {
+    if (check_norm(PE_F32, PE_F32, N, E) != PE_OK) return -1;
+    return (int64_t)std::max(norm_bwd_blocks(N, E, current_sms()), 0) * 2 * E * (int64_t)sizeof(float);
+}
+
+pe_status pe_layernorm_backward(const void *dy, const void *x, pe_dtype dt, int64_t N, int E, const void *gamma,
+                                pe_dtype w_dt, const float *mean, const float *rstd, void *dx, void *dgamma,
+                                void *dbeta, void *ws, int64_t ws_bytes, pe_stream_t stream) {
+    NvtxRange nvtx("pe_layernorm_backward");
+    if ((dgamma == nullptr) != (dbeta == nullptr)) return PE_ERR_INVALID_ARG;
+    if (pe_status s = check_norm(dt, w_dt, N, E); s != PE_OK) return s;
+    if (N > 0 && (!dy || !x || !mean || !rstd || !dx)) return PE_ERR_INVALID_ARG;
+    for (const void *p : {dy, x, gamma, (const void *)dx, (const void *)dgamma, (const void *)dbeta, (const void *)ws})
+        if (!aligned16(p)) return PE_ERR_ALIGN;
+    if (!aligned_to(mean, 4) || !aligned_to(rstd, 4)) return PE_ERR_ALIGN;
+    const int sms = current_sms();
+    if (sms < 1) return PE_ERR_CUDA;
+    const int blocks = norm_bwd_blocks(N, E, sms);
+    if (dgamma && N > 0) {
+        if (!ws) return PE_ERR_INVALID_ARG;
+        if (ws_bytes < (int64_t)blocks * 2 * E * (int64_t)sizeof(float)) return PE_ERR_SHAPE;
+    }
+    NormParams P;
+    std::memset(&P, 0, sizeof(P));
+    P.x = x;
+    P.dy = dy;
+    P.gamma = gamma;
+    P.y = dx;
+    P.mean = const_cast<float *>(mean);
+    P.rstd = const_cast<float *>(rstd);
+    P.part = dgamma ? static_cast<float *>(ws) : nullptr;
+    P.N = N;
+    P.E = E;
+    P.w_f32 = w_dt == PE_F32;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (N > 0) {
+        const cudaError_t e = dt == PE_F32 ? dispatch_norm<float>(P, true, blocks, st)
+                                           : dispatch_norm<__nv_bfloat16>(P, true, blocks, st);
+        if (e != cudaSuccess) return PE_ERR_CUDA;
+    }
+    if (!dgamma) return PE_OK;
+    pe_norm_sum_kernel<<<(2 * E + 31) / 32, 256, 0, st>>>(P.part, blocks, E, P.w_f32, dgamma, dbeta);
+    return finish(cudaGetLastError());
+}
+
+pe_status pe_attention_create(int Hq, int Hkv, int D, float scale, int causal, pe_attention **out) {
+    if (!out) return PE_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (Hq < 1 || Hkv < 1 || Hq % Hkv || D < 8 || D % 8 || !(scale > 0.f) || !std::isfinite(scale) ||
+        (causal != 0 && causal != 1))
+        return PE_ERR_INVALID_ARG;
+    if (D > 128 || Hq > 65535) return PE_ERR_UNSUPPORTED;
+    pe_attention *a = new (std::nothrow) pe_attention();
+    if (!a) return PE_ERR_HOST_MEMORY;
+    int major = 0, minor = 0;
+    if (cudaGetDevice(&a->dev) != cudaSuccess) { delete a; return PE_ERR_CUDA; }
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, a->dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, a->dev);
+    if (major != 10 || minor != 0) { delete a; return PE_ERR_UNSUPPORTED; }
+    cudaDeviceGetAttribute(&a->num_sms, cudaDevAttrMultiProcessorCount, a->dev);
+    a->Hq = Hq;
+    a->Hkv = Hkv;
+    a->D = D;
+    a->scale = scale;
+    a->causal = causal;
+    if (cudaMalloc(&a->err, sizeof(int)) != cudaSuccess || cudaMemset(a->err, 0, sizeof(int)) != cudaSuccess) {
+        pe_attention_destroy(a);
+        return PE_ERR_CUDA;
+    }
+    *out = a;
+    return PE_OK;
+}
+
+void pe_attention_destroy(pe_attention *a) {
+    if (!a) return;
+    DeviceGuard g(a->dev);
+    cudaDeviceSynchronize();
+    if (a->err) cudaFree(a->err);
+    delete a;
+}
+
+pe_status pe_attention_last_error(pe_attention *a) {
+    if (!a) return PE_ERR_INVALID_ARG;
+    DeviceGuard g(a->dev);
+    int v = 0;
+    if (cudaMemcpy(&v, a->err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return PE_ERR_CUDA;
+    if (v != 0 && cudaMemset(a->err, 0, sizeof(int)) != cudaSuccess) return PE_ERR_CUDA;
+    return v == 0 ? PE_OK : (pe_status)v;
+}
+
+int64_t pe_attention_workspace(const pe_attention *a, int n_seq, int64_t Nq, int64_t Nk, int backward) {
+    if (check_attention(a, n_seq, Nq, Nk) != PE_OK || (backward != 0 && backward != 1)) return -1;
+    return backward ? (int64_t)a->Hq * Nq * (int64_t)sizeof(float) : 0;
+}
+
+static AttnParams attention_params(const pe_attention *a, int n_seq, const int32_t *cu_q, int64_t Nq,
+                                   const int32_t *cu_k, int64_t Nk) {
+    AttnParams P;
+    std::memset(&P, 0, sizeof(P));
+    P.cu_q = cu_q;
+    P.cu_k = cu_k;
+    P.n_seq = n_seq;
+    P.Nq = (int)Nq;
+    P.Nk = (int)Nk;
+    P.Hq = a->Hq;
+    P.Hkv = a->Hkv;
+    P.D = a->D;
+    P.causal = a->causal;
+    P.scale = a->scale;
+    P.err = a->err;
+    return P;
+}
+
+pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, int64_t Nq, const int32_t *cu_k,
+                               int64_t Nk, pe_heads q, pe_heads k, pe_heads v, pe_heads out, float *lse, void *ws,
+                               int64_t ws_bytes, pe_stream_t stream) {
+    NvtxRange nvtx("pe_attention_forward");
+    if (pe_status s = check_attention(a, n_seq, Nq, Nk); s != PE_OK) return s;
+    if (n_seq == 0 || Nq == 0) return PE_OK;
+    if (!cu_q || !cu_k) return PE_ERR_INVALID_ARG;
+    if (!aligned_to(cu_q, 4) || !aligned_to(cu_k, 4) || !aligned_to(lse, 4)) return PE_ERR_ALIGN;
+    const int D = a->D;
+    for (const pe_status s : {check_heads(q, Nq, a->Hq, D), check_heads(out, Nq, a->Hq, D)})
+        if (s != PE_OK) return s;
+    if (Nk > 0)
+        for (const pe_status s : {check_heads(k, Nk, a->Hkv, D), check_heads(v, Nk, a->Hkv, D)})
+            if (s != PE_OK) return s;
+    DeviceGuard g(a->dev);
+    AttnParams P = attention_params(a, n_seq, cu_q, Nq, cu_k, Nk);
+    P.q = heads_ptr(q, Nq, a->Hq);
+    P.out = heads_ptr(out, Nq, a->Hq);
+    P.k = heads_ptr(k, Nk, a->Hkv);
+    P.v = heads_ptr(v, Nk, a->Hkv);
+    P.lse = lse;
+    pe_attn_fwd_simple<<<dim3((unsigned)((Nq + 7) / 8), (unsigned)a->Hq), 256, 0, (cudaStream_t)stream>>>(P);
+    return finish(cudaGetLastError());
+}
+
+pe_status pe_attention_backward(pe_attention *a, int n_seq, const int32_t *cu_q, int64_t Nq, const int32_t *cu_k,
+                                int64_t Nk, pe_heads q, pe_heads k, pe_heads v, pe_heads out, const float *lse,
+                                pe_heads dout, pe_heads dq, pe_heads dk, pe_heads dv, void *ws, int64_t ws_bytes,
+                                pe_stream_t stream) {
+    NvtxRange nvtx("pe_attention_backward");
+    if (pe_status s = check_attention(a, n_seq, Nq, Nk); s != PE_OK) return s;
+    if (n_seq == 0 || (Nq == 0 && Nk == 0)) return PE_OK;
+    if (!cu_q || !cu_k) return PE_ERR_INVALID_ARG;
+    if (!aligned_to(cu_q, 4) || !aligned_to(cu_k, 4) || !aligned_to(lse, 4)) return PE_ERR_ALIGN;
+    const int D = a->D;
+    if (Nq > 0) {
+        if (!lse || !ws) return PE_ERR_INVALID_ARG;
+        if (!aligned16(ws)) return PE_ERR_ALIGN;
+        if (ws_bytes < pe_attention_workspace(a, n_seq, Nq, Nk, 1)) return PE_ERR_SHAPE;
+        for (const pe_status s : {check_heads(q, Nq, a->Hq, D), check_heads(out, Nq, a->Hq, D),
+                                  check_heads(dout, Nq, a->Hq, D), check_heads(dq, Nq, a->Hq, D)})
+            if (s != PE_OK) return s;
+    }
+    if (Nk > 0)
+        for (const pe_status s : {check_heads(k, Nk, a->Hkv, D), check_heads(v, Nk, a->Hkv, D),
+                                  check_heads(dk, Nk, a->Hkv, D), check_heads(dv, Nk, a->Hkv, D)})
+            if (s != PE_OK) return s;
+    DeviceGuard g(a->dev);
+    AttnParams P = attention_params(a, n_seq, cu_q, Nq, cu_k, Nk);
+    P.q = heads_ptr(q, Nq, a->Hq);
+    P.out = heads_ptr(out, Nq, a->Hq);
+    P.dout = heads_ptr(dout, Nq, a->Hq);
+    P.dq = heads_ptr(dq, Nq, a->Hq);
+    P.k = heads_ptr(k, Nk, a->Hkv);
+    P.v = heads_ptr(v, Nk, a->Hkv);
+    P.dk = heads_ptr(dk, Nk, a->Hkv);
+    P.dv = heads_ptr(dv, Nk, a->Hkv);
+    P.lse = const_cast<float *>(lse);
+    P.delta = static_cast<float *>(ws);
+    cudaStream_t st = (cudaStream_t)stream;
+    if (Nq > 0) {
+        pe_attn_dq_simple<<<dim3((unsigned)((Nq + 7) / 8), (unsigned)a->Hq), 256, 0, st>>>(P);
+        if (cudaGetLastError() != cudaSuccess) return PE_ERR_CUDA;
+    }
+    if (Nk == 0) return PE_OK;
+    pe_attn_dkv_simple<<<dim3((unsigned)((Nk + 7) / 8), (unsigned)a->Hkv), 256, 0, st>>>(P);
+    return finish(cudaGetLastError());
+}
+
+}  // extern "C"
