@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstring>
 #include <new>
+#include <type_traits>
 
 #include "../../include/pe.h"
 #include "pe_attention.cuh"
@@ -141,6 +142,33 @@ pe_status check_heads(const pe_heads &t, int64_t rows, int heads, int D) {
 HeadsPtr heads_ptr(const pe_heads &t, int64_t rows, int heads) {
     return {static_cast<__nv_bfloat16 *>(t.ptr), rows > 1 ? t.row_stride : 0, heads > 1 ? t.head_stride : 0};
 }
+
+// [rows, heads, D] bf16 in boxes of 128 rows of one head and 64 elements, 128-byte
+// swizzle; what lies outside reads as zero.
+bool make_heads_tmap(CUtensorMap *m, const pe_heads &t, int64_t rows, int heads, int D) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const int64_t row = rows > 1 ? t.row_stride : (int64_t)heads * D, head = heads > 1 ? t.head_stride : D;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)head * 2, (cuuint64_t)row * 2};
+    cuuint32_t box[3] = {64, 1, kTile}, estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Calls f(std::integral_constant<int, DP>) with the head size rounded up to one
+// the kernels are compiled for.
+template <class F>
+auto with_head_size(int D, F &&f) {
+    if (D <= 64) return f(std::integral_constant<int, 64>());
+    if (D <= 80) return f(std::integral_constant<int, 80>());
+    if (D <= 96) return f(std::integral_constant<int, 96>());
+    return f(std::integral_constant<int, 128>());
+}
+
+// Tiles of `rows` rows that n rows in n_seq sequences can make, at most.
+unsigned max_tiles(int64_t n, int n_seq, int rows) { return (unsigned)(n / rows + std::min<int64_t>(n_seq, n)); }
 
 // Sizes that do not depend on the buffers.
 pe_status check_attention(const pe_attention *a, int n_seq, int64_t Nq, int64_t Nk) {
@@ -409,8 +437,20 @@ pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, 
     P.k = heads_ptr(k, Nk, a->Hkv);
     P.v = heads_ptr(v, Nk, a->Hkv);
     P.lse = lse;
-    pe_attn_fwd_simple<<<dim3((unsigned)((Nq + 7) / 8), (unsigned)a->Hq), 256, 0, (cudaStream_t)stream>>>(P);
-    return finish(cudaGetLastError());
+    // without keys no map is read: any valid tensor stands in
+    CUtensorMap mq, mk, mv;
+    if (!make_heads_tmap(&mq, q, Nq, a->Hq, D) || !make_heads_tmap(&mk, Nk ? k : q, Nk ? Nk : Nq, Nk ? a->Hkv : a->Hq, D) ||
+        !make_heads_tmap(&mv, Nk ? v : q, Nk ? Nk : Nq, Nk ? a->Hkv : a->Hq, D))
+        return PE_ERR_CUDA;
+    const dim3 grid(max_tiles(Nq, n_seq, 2 * kTile), (unsigned)a->Hq);
+    return with_head_size(D, [&](auto dp) {
+        constexpr int DP = decltype(dp)::value;
+        auto kern = pe_attn_fwd_kernel<DP>;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFwdSmem<DP>) != cudaSuccess)
+            return PE_ERR_CUDA;
+        kern<<<grid, kFwdThreads, kFwdSmem<DP>, (cudaStream_t)stream>>>(mq, mk, mv, P);
+        return finish(cudaGetLastError());
+    });
 }
 
 pe_status pe_attention_backward(pe_attention *a, int n_seq, const int32_t *cu_q, int64_t Nq, const int32_t *cu_k,
