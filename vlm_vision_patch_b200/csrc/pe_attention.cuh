@@ -101,7 +101,7 @@ struct AttnParams {
     float scale;
     HeadsPtr q, k, v, out, dout, dq, dk, dv;
     float *lse;                   // [Hq, Nq]
-    float *delta;                 // [Hq, Nq]
+    float *lse2, *delta;          // [Hq, Nq]: lse * log2(e), and dout . out (backward)
     int *err;
 };
 
@@ -109,36 +109,6 @@ struct AttnParams {
 __device__ __forceinline__ int boundary(const int32_t *cu, int s, int n) {
     const int v = cu[s];
     return v < 0 ? 0 : (v > n ? n : v);
-}
-
-// The last sequence that begins at or before row r, or -1.
-__device__ __forceinline__ int sequence_of(const int32_t *cu, int n_seq, int r) {
-    int lo = -1, hi = n_seq - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cu[mid] <= r) lo = mid; else hi = mid - 1;
-    }
-    return lo;
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
-// Four elements of a head per lane (D <= 128, a multiple of 8).
-__device__ __forceinline__ void lane_load(const __nv_bfloat16 *p, int D, int lane, float (&v)[4]) {
-    uint2 w = make_uint2(0, 0);
-    if (4 * lane < D) w = *reinterpret_cast<const uint2 *>(p + 4 * lane);
-    v[0] = bf16lo_to_f32(w.x), v[1] = bf16hi_to_f32(w.x), v[2] = bf16lo_to_f32(w.y), v[3] = bf16hi_to_f32(w.y);
-}
-__device__ __forceinline__ void lane_store(__nv_bfloat16 *p, int D, int lane, const float (&v)[4], float f) {
-    if (4 * lane < D)
-        *reinterpret_cast<uint2 *>(p + 4 * lane) = make_uint2(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f));
-}
-__device__ __forceinline__ float dot4(const float (&a)[4], const float (&b)[4]) {
-    return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3];
 }
 
 // ------------------------------------------------------------- tiles and work
@@ -199,21 +169,23 @@ __device__ __forceinline__ int keys_seen(const AttnParams &P, const Work &w, int
 // rows behind its sequence's end meet probabilities of 0, but they belong to
 // whatever lies there, and 0 * NaN is not 0.  The swizzle permutes 16-byte
 // groups within a row, so whole rows need no index arithmetic.
-template <int CHUNKS>
+template <int CHUNKS, int CHUNK>
 __device__ __forceinline__ void zero_rows(uint8_t *tile, int valid, int end) {
     const int groups = (end - valid) * 8;
     for (int c = 0; c < CHUNKS; ++c)
         for (int i = threadIdx.x & 31; i < groups; i += 32)
-            *reinterpret_cast<uint4 *>(tile + c * kChunkBytes + valid * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(tile + c * CHUNK + valid * 128 + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
-// K-major operand (rows x 64-column chunks), k-step of 16 columns.
+// K-major operand (chunks of 64 columns, CHUNK bytes each), k-step of 16 columns.
+template <int CHUNK>
 __device__ __forceinline__ uint64_t desc_k(uint32_t tile, int kstep) {
-    return smem_desc(tile + (kstep >> 2) * kChunkBytes + (kstep & 3) * 32, 16, 1024, kLayoutSw128);
+    return smem_desc(tile + (kstep >> 2) * CHUNK + (kstep & 3) * 32, 16, 1024, kLayoutSw128);
 }
 // The same tile read along its rows (MN-major): k-step of 16 rows, N = the columns.
+template <int CHUNK>
 __device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int kstep) {
-    return smem_desc(tile + kstep * 2048, kChunkBytes, 1024, kLayoutSw128);
+    return smem_desc(tile + kstep * 2048, CHUNK, 1024, kLayoutSw128);
 }
 __host__ __device__ constexpr uint32_t idesc_b_mn(int M, int N) { return idesc_bf16_f32(M, N) | (1u << 16); }
 
@@ -429,7 +401,7 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                     mbar_wait(smem_addr(&B.tail), 0, &never);
                     break;
                 }
-                zero_rows<kC>(dst, valid, (valid + 15) & ~15);
+                zero_rows<kC, kChunkBytes>(dst, valid, (valid + 15) & ~15);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&B.full[slot]));
@@ -452,8 +424,8 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         };
         auto issue_s = [&](int t, int f) {
             for (int k = 0; k < ksteps; ++k)
-                mma_ss(B.tmem + t * 128, desc_k(a_q + t * kTileBytes, k), desc_k(a_r + f % kFwdStages * kTileBytes, k), kIdS,
-                       k > 0);
+                mma_ss(B.tmem + t * 128, desc_k<kChunkBytes>(a_q + t * kTileBytes, k),
+                       desc_k<kChunkBytes>(a_r + f % kFwdStages * kTileBytes, k), kIdS, k > 0);
             mma_commit(&B.s_full[t]);
         };
         bool ok = mbar_wait(smem_addr(&B.qfull), 0, abort) && wait_full(0);
@@ -476,7 +448,7 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                     const int psteps = (rows + 15) / 16;
                     for (int k = 0; k < psteps; ++k)
                         mma_ts(B.tmem + 256 + t * 128, B.tmem + t * 128 + 8 * k,
-                               desc_mn(a_r + fv % kFwdStages * kTileBytes, k), kIdO, j > 0 || k > 0);
+                               desc_mn<kChunkBytes>(a_r + fv % kFwdStages * kTileBytes, k), kIdO, j > 0 || k > 0);
                     if (j + 1 == n_kv[t]) mma_commit(&B.o_full[t]);
                 }
                 if (j + 1 < n_kv[t]) issue_s(t, fk);
@@ -502,68 +474,346 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
 }
 
 // ------------------------------------------------------------- backward
+//
+// Two kernels of one shape, so that no sum needs atomics and two runs give the
+// same bits: one block keeps 128 query rows and streams the keys past them (dq),
+// then one block keeps 128 key rows and streams the queries past them (dk, dv).
+// Both recompute the scores; that is 7 products of a tile pair instead of 5, and
+// in exchange dq is summed in tensor memory rather than in fp32 in HBM.
+//
+// With x0, x1 the kept rows and y0, y1 the streamed ones (q, dout and k, v, or
+// k, v and q, dout):   s = x0 y0^T,  dp = x1 y1^T,  p = exp(s - lse),
+// ds = p (dp - delta);  kept rows += ds y0, and for keys also p y1.
+// The streamed tiles hold 64 rows, so that two pairs (s, dp) fit in tensor
+// memory beside the sums: warps 0-3 work on one while the tensor cores fill the
+// other for warps 4-7.  p and ds go back to tensor memory as bf16 and are the A
+// operands of the sums.
 
-// delta and dq: one warp per query row and head.
-__global__ void pe_attn_dq_simple(const AttnParams P) {
-    const int lane = threadIdx.x & 31, r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), h = blockIdx.y;
-    if (r >= P.Nq) return;
-    const int s = sequence_of(P.cu_q, P.n_seq, r);
-    if (s < 0) return;
-    const int q0 = boundary(P.cu_q, s, P.Nq), q1 = boundary(P.cu_q, s + 1, P.Nq);
-    const int k0 = boundary(P.cu_k, s, P.Nk), k1 = boundary(P.cu_k, s + 1, P.Nk);
-    if (r >= q1) return;
-    const int lk = k1 > k0 ? k1 - k0 : 0;
-    int limit = lk;
-    if (P.causal) limit = min(lk, max(0, r - q0 + 1 + lk - (q1 - q0)));
-    const int hk = h / (P.Hq / P.Hkv);
-    float q[4], o[4], g[4], dq[4] = {0.f, 0.f, 0.f, 0.f};
-    lane_load(P.q.at(r, h), P.D, lane, q);
-    lane_load(P.out.at(r, h), P.D, lane, o);
-    lane_load(P.dout.at(r, h), P.D, lane, g);
-    const float delta = warp_sum(dot4(g, o)), lse = P.lse[(int64_t)h * P.Nq + r];
-    if (lane == 0) P.delta[(int64_t)h * P.Nq + r] = delta;
-    for (int j = 0; j < limit; ++j) {
-        float k[4], v[4];
-        lane_load(P.k.at(k0 + j, hk), P.D, lane, k);
-        lane_load(P.v.at(k0 + j, hk), P.D, lane, v);
-        const float p = __expf(warp_sum(dot4(q, k)) * P.scale - lse), ds = p * (warp_sum(dot4(g, v)) - delta);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dq[e] += ds * k[e];
-    }
-    lane_store(P.dq.at(r, h), P.D, lane, dq, P.scale);
+constexpr int kStream = 64;                       // streamed rows per tile
+constexpr int kStreamChunk = kStream * 128;       // bytes of 64 rows of 64 bf16
+constexpr int kBwdThreads = 320;
+constexpr int kBwdStages = 4;
+
+template <int DP>
+constexpr size_t kBwdSmem = (size_t)kChunks<DP> * (2 * kChunkBytes + kBwdStages * 2 * kStreamChunk) + 1024;
+
+struct BwdBars {
+    uint64_t full[kBwdStages], empty[kBwdStages], tail, xfull, s_full[2], d_full[2], acc_full, drain;
+    uint32_t tmem;
+    int abort;
+    Work w;
+    alignas(16) float stat[kBwdStages][2][kStream];   // lse2 and delta of the streamed queries
+};
+
+// 4 bytes to shared memory without waiting; zero when !take.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float *src, bool take) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(take ? 4 : 0) : "memory");
+}
+// This thread's copies so far, once they have landed, count as one arrival.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// dk and dv: one warp per key row and key head, over the rows that see it and
-// the query heads that share it.
-__global__ void pe_attn_dkv_simple(const AttnParams P) {
-    const int lane = threadIdx.x & 31, r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), hk = blockIdx.y;
-    if (r >= P.Nk) return;
-    const int s = sequence_of(P.cu_k, P.n_seq, r);
-    if (s < 0) return;
-    const int q0 = boundary(P.cu_q, s, P.Nq), q1 = boundary(P.cu_q, s + 1, P.Nq);
-    const int k0 = boundary(P.cu_k, s, P.Nk), k1 = boundary(P.cu_k, s + 1, P.Nk);
-    if (r >= k1) return;
-    int first = 0;
-    if (P.causal) first = max(0, r - k0 - ((k1 - k0) - (q1 - q0)));
-    float k[4], v[4], dk[4] = {0.f, 0.f, 0.f, 0.f}, dv[4] = {0.f, 0.f, 0.f, 0.f};
-    lane_load(P.k.at(r, hk), P.D, lane, k);
-    lane_load(P.v.at(r, hk), P.D, lane, v);
-    const int share = P.Hq / P.Hkv;
-    for (int h = hk * share; h < (hk + 1) * share; ++h)
-        for (int i = q0 + first; i < q1; ++i) {
-            float q[4], g[4];
-            lane_load(P.q.at(i, h), P.D, lane, q);
-            lane_load(P.dout.at(i, h), P.D, lane, g);
-            const float p = __expf(warp_sum(dot4(q, k)) * P.scale - P.lse[(int64_t)h * P.Nq + i]);
-            const float ds = p * (warp_sum(dot4(g, v)) - P.delta[(int64_t)h * P.Nq + i]);
+// The streamed tiles of one block: for keys, the query tiles of every head that
+// shares the key head, from the first that sees the tile's first key.
+struct Stream {
+    int first, per_head, n;                       // first tile, tiles per head, tiles in all
+};
+
+template <bool KEYS>
+__device__ __forceinline__ Stream stream_of(const AttnParams &P, const Work &w) {
+    Stream st = {0, 0, 0};
+    if (KEYS) {
+        const int i0 = P.causal ? max(0, w.row - (w.lk - w.lq)) : 0;
+        st.first = i0 / kStream;
+        st.per_head = max((w.lq + kStream - 1) / kStream - st.first, 0);
+        st.n = st.per_head * (P.Hq / P.Hkv);
+    } else {
+        const int last = min(w.row + kTile, w.lq) - 1;
+        st.per_head = st.n = (keys_seen(P, w, last) + kStream - 1) / kStream;
+    }
+    return st;
+}
+
+// p and ds of every second streamed tile, then half of the results; the 128
+// threads of group g, one kept row each.
+template <int DP, bool KEYS>
+__device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const Work &w, const Stream &st, int g, int h) {
+    volatile int *abort = &B.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t ts = B.tmem + lanes + g * 128, td = ts + 64;
+    const int i = w.row + (warp & 3) * 32 + lane;           // kept row within the sequence
+    const bool mine = i < (KEYS ? w.lk : w.lq);
+    const float sl2 = P.scale * kLog2e;
+    float lse2 = 0.f, delta = 0.f;
+    int limit = 0;
+    if (!KEYS) {
+        limit = mine ? keys_seen(P, w, i) : 0;
+        if (mine) {
+            const int64_t row = w.q0 + i, at = (int64_t)h * P.Nq + row;
+            const __nv_bfloat16 *a = P.dout.at(row, h), *b = P.out.at(row, h);
+            for (int e = 0; e < P.D; e += 8) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(a + e), v = *reinterpret_cast<const uint4 *>(b + e);
+                const uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                dv[e] += p * g[e];
-                dk[e] += ds * q[e];
+                for (int k = 0; k < 4; ++k)
+                    delta += bf16lo_to_f32(x[k]) * bf16lo_to_f32(y[k]) + bf16hi_to_f32(x[k]) * bf16hi_to_f32(y[k]);
+            }
+            // a row that sees no key has lse = -inf; +inf gives it p = 0 for every key
+            lse2 = limit > 0 ? P.lse[at] * kLog2e : INFINITY;
+            if (g == 0) {
+                P.lse2[at] = lse2;
+                P.delta[at] = delta;
             }
         }
-    lane_store(P.dk.at(r, hk), P.D, lane, dk, P.scale);
-    lane_store(P.dv.at(r, hk), P.D, lane, dv, 1.0f);
+    }
+    const int shift = w.lk - w.lq;
+    for (int j = g; j < st.n; j += 2) {
+        const int n = j >> 1, stage = j % kBwdStages;
+        if (KEYS && !warp_wait(&B.full[stage], (j / kBwdStages) & 1, abort)) return;
+        if (!warp_wait(&B.s_full[g], n & 1, abort)) return;
+        tc_fence_after();
+        const int y = (st.first + (KEYS ? j % st.per_head : j)) * kStream;      // first streamed row
+        uint32_t s[2][32], d[2][32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            tmem_ld_32x32b_x32(ts + 32 * c, s[c]);
+            tmem_ld_32x32b_x32(td + 32 * c, d[c]);
+        }
+        tmem_ld_wait();
+        // queries a key row sees start at i - shift; keys a query row sees end at limit
+        const bool cut = __any_sync(0xffffffffu, KEYS ? P.causal && y < i - shift : y + kStream > limit);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            uint32_t pp[16], pd[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+                float4 L = make_float4(lse2, lse2, lse2, lse2), T = make_float4(delta, delta, delta, delta);
+                if (KEYS) {
+                    L = *reinterpret_cast<const float4 *>(&B.stat[stage][0][32 * c + e]);
+                    T = *reinterpret_cast<const float4 *>(&B.stat[stage][1][32 * c + e]);
+                }
+                const float l4[4] = {L.x, L.y, L.z, L.w}, t4[4] = {T.x, T.y, T.z, T.w};
+                float p[4], q[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    p[k] = ex2(fmaf(__uint_as_float(s[c][e + k]), sl2, -l4[k]));
+                    q[k] = p[k] * (__uint_as_float(d[c][e + k]) - t4[k]);
+                    if (cut) {
+                        const int col = y + 32 * c + e + k;
+                        if (KEYS ? col < i - shift : col >= limit) p[k] = q[k] = 0.f;
+                    }
+                }
+                pp[e / 2] = pack_bf16x2(p[0], p[1]);
+                pp[e / 2 + 1] = pack_bf16x2(p[2], p[3]);
+                pd[e / 2] = pack_bf16x2(q[0], q[1]);
+                pd[e / 2 + 1] = pack_bf16x2(q[2], q[3]);
+            }
+            if (KEYS) tmem_st_x16(ts + 16 * c, pp);
+            tmem_st_x16(td + 16 * c, pd);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&B.d_full[g]));
+    }
+    if (st.n > 0) {
+        if (!warp_wait(&B.acc_full, 0, abort)) return;
+        tc_fence_after();
+    }
+    // keys: group 0 writes dv, group 1 dk; queries: every second 16 columns of dq
+    const bool is_dv = KEYS && g == 0;
+    const uint32_t acc = B.tmem + lanes + (is_dv ? 256 : 384);
+    const float f = is_dv ? 1.0f : P.scale;
+    __nv_bfloat16 *out = KEYS ? (is_dv ? P.dv : P.dk).at(w.k0 + i, h) : P.dq.at(w.q0 + i, h);
+#pragma unroll
+    for (int c = 0; c < DP / 16; ++c) {
+        if (!KEYS && (c & 1) != g) continue;
+        uint32_t o[16] = {0};
+        if (st.n > 0) {
+            tmem_ld_x16(acc + 16 * c, o);
+            tmem_ld_wait();
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                pk[e] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * e]) * f, __uint_as_float(o[8 * q + 2 * e + 1]) * f);
+            if (mine && 16 * c + 8 * q < P.D) st_global_v4(out + 16 * c + 8 * q, pk[0], pk[1], pk[2], pk[3]);
+        }
+    }
+}
+
+// mx0, mx1: maps of the kept tensors, my0, my1 of the streamed ones (boxes of 64 rows).
+template <int DP, bool KEYS>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constant__ CUtensorMap mx1,
+                   const __grid_constant__ CUtensorMap my0, const __grid_constant__ CUtensorMap my1,
+                   const __grid_constant__ AttnParams P) {
+    constexpr int kC = kChunks<DP>;
+    constexpr uint32_t kKept = kC * kChunkBytes, kOne = kC * kStreamChunk;     // bytes of one kept / streamed tile
+    extern __shared__ uint8_t raw[];
+    __shared__ BwdBars B;
+    uint8_t *kept = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023), *ring = kept + 2 * kKept;
+    volatile int *abort = &B.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.y, share = P.Hq / P.Hkv;
+    if (warp == 9) {
+        const Work w = find_work(P, KEYS, blockIdx.x, kTile);
+        if (lane == 0) {
+            B.w = w;
+            B.abort = 0;
+            for (int i = 0; i < kBwdStages; ++i) {
+                mbar_init(smem_addr(&B.full[i]), KEYS ? 33 : 1);
+                mbar_init(smem_addr(&B.empty[i]), 1);
+            }
+            mbar_init(smem_addr(&B.tail), 1);
+            mbar_init(smem_addr(&B.xfull), 1);
+            mbar_init(smem_addr(&B.acc_full), 1);
+            mbar_init(smem_addr(&B.drain), 1);
+            for (int t = 0; t < 2; ++t) mbar_init(smem_addr(&B.s_full[t]), 1), mbar_init(smem_addr(&B.d_full[t]), 4);
+            fence_mbar_init();
+            prefetch_tmap(&mx0);
+            prefetch_tmap(&mx1);
+            prefetch_tmap(&my0);
+            prefetch_tmap(&my1);
+        }
+    }
+    __syncthreads();
+    const Work w = B.w;
+    if (w.row < 0) return;
+    if (warp == 8) {
+        tmem_alloc(smem_addr(&B.tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const Stream st = stream_of<KEYS>(P, w);
+    const int y_len = KEYS ? w.lq : w.lk;                   // streamed rows of the sequence
+    if (warp < 8) {
+        bwd_group<DP, KEYS>(P, B, w, st, warp >> 2, h);
+    } else if (warp == 8 && st.n > 0) {
+        // ---- loads
+        const int x_row = (KEYS ? w.k0 : w.q0) + w.row, x_head = h;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(smem_addr(&B.xfull), 2 * kKept);
+            for (int t = 0; t < 2; ++t)
+                for (int c = 0; c < kC; ++c)
+                    for (int half = 0; half < 2; ++half)
+                        tma_load_3d(smem_addr(kept + t * kKept + c * kChunkBytes + half * kStreamChunk), t ? &mx1 : &mx0,
+                                    smem_addr(&B.xfull), 64 * c, x_head, x_row + half * kStream);
+        }
+        int f = 0, tails = 0;
+        bool ok = true;
+        for (; f < st.n; ++f) {
+            const int slot = f % kBwdStages;
+            ok = warp_wait(&B.empty[slot], ((f / kBwdStages) & 1) ^ 1, abort);
+            if (!ok) break;
+            const int row = (st.first + (KEYS ? f % st.per_head : f)) * kStream;
+            const int y_head = KEYS ? h * share + f / st.per_head : h / share;
+            const int y_row = (KEYS ? w.q0 : w.k0) + row;
+            const int valid = min(y_len - row, kStream);
+            uint8_t *dst = ring + slot * 2 * kOne;
+            const bool clean = valid < kStream;             // the sequence's last tile: zeros behind it
+            uint64_t *bar = clean ? &B.tail : &B.full[slot];
+            if (KEYS) {
+                const float *src = P.lse2 + (int64_t)y_head * P.Nq + y_row;
+                const float *srd = P.delta + (int64_t)y_head * P.Nq + y_row;
+#pragma unroll
+                for (int e = lane; e < kStream; e += 32) {
+                    const bool in = e < valid;
+                    cp_async4(smem_addr(&B.stat[slot][0][e]), in ? src + e : src, in);
+                    cp_async4(smem_addr(&B.stat[slot][1][e]), in ? srd + e : srd, in);
+                }
+                cp_async_arrive(smem_addr(&B.full[slot]));
+            }
+            if (lane == 0) {
+                mbar_arrive_expect_tx(smem_addr(bar), 2 * kOne);
+                for (int t = 0; t < 2; ++t)
+                    for (int c = 0; c < kC; ++c)
+                        tma_load_3d(smem_addr(dst + t * kOne + c * kStreamChunk), t ? &my1 : &my0, smem_addr(bar), 64 * c,
+                                    y_head, y_row);
+            }
+            __syncwarp();
+            if (clean) {
+                ok = warp_wait(&B.tail, tails & 1, abort);
+                if (!ok) {
+                    int never = 0;
+                    mbar_wait(smem_addr(&B.tail), tails & 1, &never);
+                    break;
+                }
+                ++tails;
+                for (int t = 0; t < 2; ++t) zero_rows<kC, kStreamChunk>(dst + t * kOne, valid, (valid + 15) & ~15);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&B.full[slot]));
+            }
+        }
+        if (!ok) {   // a wait gave up: the copies in flight still land before the block ends
+            int never = 0;
+            mbar_wait(smem_addr(&B.xfull), 0, &never);
+            for (int s = max(f - kBwdStages, 0); s < f; ++s)
+                mbar_wait(smem_addr(&B.full[s % kBwdStages]), (s / kBwdStages) & 1, &never);
+        }
+    } else if (warp == 9 && lane == 0 && st.n > 0) {
+        // ---- MMAs
+        constexpr uint32_t kIdS = idesc_bf16_f32(kTile, kStream), kIdA = idesc_b_mn(kTile, DP);
+        const int ksteps = (P.D + 15) / 16;
+        const uint32_t a0 = smem_addr(kept), r0 = smem_addr(ring);
+        auto issue_s = [&](int j) {
+            const uint32_t y = r0 + j % kBwdStages * 2 * kOne, d = B.tmem + (j & 1) * 128;
+            for (int k = 0; k < ksteps; ++k)
+                mma_ss(d, desc_k<kChunkBytes>(a0, k), desc_k<kStreamChunk>(y, k), kIdS, k > 0);
+            for (int k = 0; k < ksteps; ++k)
+                mma_ss(d + 64, desc_k<kChunkBytes>(a0 + kKept, k), desc_k<kStreamChunk>(y + kOne, k), kIdS, k > 0);
+            mma_commit(&B.s_full[j & 1]);
+        };
+        auto wait_full = [&](int f) {
+            return mbar_wait(smem_addr(&B.full[f % kBwdStages]), (f / kBwdStages) & 1, abort);
+        };
+        bool ok = mbar_wait(smem_addr(&B.xfull), 0, abort);
+        for (int j = 0; j < 2 && j < st.n && ok; ++j) {
+            ok = wait_full(j);
+            tc_fence_after();
+            if (ok) issue_s(j);
+        }
+        for (int j = 0; j < st.n && ok; ++j) {
+            const int b = j & 1, row = (st.first + (KEYS ? j % st.per_head : j)) * kStream;
+            const int steps = (min(y_len - row, kStream) + 15) / 16;
+            const uint32_t y = r0 + j % kBwdStages * 2 * kOne, d = B.tmem + b * 128;
+            ok = mbar_wait(smem_addr(&B.d_full[b]), (j >> 1) & 1, abort);
+            if (!ok) break;
+            tc_fence_after();
+            if (KEYS)
+                for (int k = 0; k < steps; ++k)
+                    mma_ts(B.tmem + 256, d + 8 * k, desc_mn<kStreamChunk>(y + kOne, k), kIdA, j > 0 || k > 0);
+            for (int k = 0; k < steps; ++k)
+                mma_ts(B.tmem + 384, d + 64 + 8 * k, desc_mn<kStreamChunk>(y, k), kIdA, j > 0 || k > 0);
+            mma_commit(&B.empty[j % kBwdStages]);
+            if (j + 1 == st.n) mma_commit(&B.acc_full);
+            if (j + 2 < st.n) {
+                ok = wait_full(j + 2);
+                tc_fence_after();
+                if (ok) issue_s(j + 2);
+            }
+        }
+        if (!ok) {   // MMAs in flight finish before their tensor memory is freed
+            int never = 0;
+            mma_commit(&B.drain);
+            mbar_wait(smem_addr(&B.drain), 0, &never);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && B.abort) atomicExch(P.err, (int)PE_ERR_DEVICE_TIMEOUT);
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(B.tmem, 512);
+    }
 }
 
 }  // namespace pe

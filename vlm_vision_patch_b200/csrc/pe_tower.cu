@@ -143,15 +143,15 @@ HeadsPtr heads_ptr(const pe_heads &t, int64_t rows, int heads) {
     return {static_cast<__nv_bfloat16 *>(t.ptr), rows > 1 ? t.row_stride : 0, heads > 1 ? t.head_stride : 0};
 }
 
-// [rows, heads, D] bf16 in boxes of 128 rows of one head and 64 elements, 128-byte
+// [rows, heads, D] bf16 in boxes of `box_rows` rows of one head and 64 elements, 128-byte
 // swizzle; what lies outside reads as zero.
-bool make_heads_tmap(CUtensorMap *m, const pe_heads &t, int64_t rows, int heads, int D) {
+bool make_heads_tmap(CUtensorMap *m, const pe_heads &t, int64_t rows, int heads, int D, uint32_t box_rows) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const int64_t row = rows > 1 ? t.row_stride : (int64_t)heads * D, head = heads > 1 ? t.head_stride : D;
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
     cuuint64_t strides[2] = {(cuuint64_t)head * 2, (cuuint64_t)row * 2};
-    cuuint32_t box[3] = {64, 1, kTile}, estr[3] = {1, 1, 1};
+    cuuint32_t box[3] = {64, 1, box_rows}, estr[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -395,7 +395,7 @@ pe_status pe_attention_last_error(pe_attention *a) {
 
 int64_t pe_attention_workspace(const pe_attention *a, int n_seq, int64_t Nq, int64_t Nk, int backward) {
     if (check_attention(a, n_seq, Nq, Nk) != PE_OK || (backward != 0 && backward != 1)) return -1;
-    return backward ? (int64_t)a->Hq * Nq * (int64_t)sizeof(float) : 0;
+    return backward ? 2 * (int64_t)a->Hq * Nq * (int64_t)sizeof(float) : 0;
 }
 
 static AttnParams attention_params(const pe_attention *a, int n_seq, const int32_t *cu_q, int64_t Nq,
@@ -437,10 +437,11 @@ pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, 
     P.k = heads_ptr(k, Nk, a->Hkv);
     P.v = heads_ptr(v, Nk, a->Hkv);
     P.lse = lse;
-    // without keys no map is read: any valid tensor stands in
+    // without keys their maps are not read
     CUtensorMap mq, mk, mv;
-    if (!make_heads_tmap(&mq, q, Nq, a->Hq, D) || !make_heads_tmap(&mk, Nk ? k : q, Nk ? Nk : Nq, Nk ? a->Hkv : a->Hq, D) ||
-        !make_heads_tmap(&mv, Nk ? v : q, Nk ? Nk : Nq, Nk ? a->Hkv : a->Hq, D))
+    if (!make_heads_tmap(&mq, q, Nq, a->Hq, D, kTile)) return PE_ERR_CUDA;
+    mk = mv = mq;
+    if (Nk > 0 && (!make_heads_tmap(&mk, k, Nk, a->Hkv, D, kTile) || !make_heads_tmap(&mv, v, Nk, a->Hkv, D, kTile)))
         return PE_ERR_CUDA;
     const dim3 grid(max_tiles(Nq, n_seq, 2 * kTile), (unsigned)a->Hq);
     return with_head_size(D, [&](auto dp) {
@@ -486,15 +487,35 @@ pe_status pe_attention_backward(pe_attention *a, int n_seq, const int32_t *cu_q,
     P.dk = heads_ptr(dk, Nk, a->Hkv);
     P.dv = heads_ptr(dv, Nk, a->Hkv);
     P.lse = const_cast<float *>(lse);
-    P.delta = static_cast<float *>(ws);
+    P.lse2 = static_cast<float *>(ws);
+    P.delta = P.lse2 + (int64_t)a->Hq * Nq;
     cudaStream_t st = (cudaStream_t)stream;
-    if (Nq > 0) {
-        pe_attn_dq_simple<<<dim3((unsigned)((Nq + 7) / 8), (unsigned)a->Hq), 256, 0, st>>>(P);
-        if (cudaGetLastError() != cudaSuccess) return PE_ERR_CUDA;
-    }
-    if (Nk == 0) return PE_OK;
-    pe_attn_dkv_simple<<<dim3((unsigned)((Nk + 7) / 8), (unsigned)a->Hkv), 256, 0, st>>>(P);
-    return finish(cudaGetLastError());
+    CUtensorMap mq, mk, mv, md;
+    if (Nq > 0 && (!make_heads_tmap(&mq, q, Nq, a->Hq, D, kStream) || !make_heads_tmap(&md, dout, Nq, a->Hq, D, kStream)))
+        return PE_ERR_CUDA;
+    if (Nk > 0 && (!make_heads_tmap(&mk, k, Nk, a->Hkv, D, kStream) || !make_heads_tmap(&mv, v, Nk, a->Hkv, D, kStream)))
+        return PE_ERR_CUDA;
+    // the maps of a side without rows are not read
+    if (Nq == 0) mq = mk, md = mv;
+    if (Nk == 0) mk = mq, mv = md;
+    return with_head_size(D, [&](auto dp) {
+        constexpr int DP = decltype(dp)::value;
+        auto dq_kern = pe_attn_bwd_kernel<DP, false>;
+        auto dkv_kern = pe_attn_bwd_kernel<DP, true>;
+        for (auto kern : {dq_kern, dkv_kern})
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBwdSmem<DP>) != cudaSuccess)
+                return PE_ERR_CUDA;
+        if (Nq > 0) {
+            const dim3 grid(max_tiles(Nq, n_seq, kTile), (unsigned)a->Hq);
+            dq_kern<<<grid, kBwdThreads, kBwdSmem<DP>, st>>>(mq, md, mk, mv, P);
+            if (cudaGetLastError() != cudaSuccess) return PE_ERR_CUDA;
+        }
+        if (Nk > 0) {
+            const dim3 grid(max_tiles(Nk, n_seq, kTile), (unsigned)a->Hkv);
+            dkv_kern<<<grid, kBwdThreads, kBwdSmem<DP>, st>>>(mk, mv, mq, md, P);
+        }
+        return finish(cudaGetLastError());
+    });
 }
 
 }  // extern "C"
