@@ -16,9 +16,26 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// mbar_wait for barriers that only this block arrives on (block-scope acquire),
+// on the critical path of a softmax: the clock is read only once the wait has
+// failed a few times.
+__device__ __forceinline__ bool block_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    }
+    return mbar_wait(smem_addr(bar), parity, abort);
+}
 // A whole warp waits; all lanes go on, or none (a wait gave up).
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    return __all_sync(0xffffffffu, mbar_wait(smem_addr(bar), parity, abort));
+    return __all_sync(0xffffffffu, block_wait(bar, parity, abort));
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int32_t x, int32_t y,
@@ -41,23 +58,39 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
+// Registers per thread from here on, for the four warps of a warpgroup.
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p;
+}
+
+// Descriptors are passed as (low word, high word): a tile's k-step only changes the
+// low word, and the issuing thread has little time per MMA.
 // D[tmem] (+)= A[smem] B[smem]
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi_a, uint32_t hi_b, uint32_t idesc,
+                                       bool acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 x, {%1, %3};\n\t"
+        "mov.b64 y, {%2, %4};\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(hi_a), "r"(hi_b), "r"(idesc), "r"((uint32_t)acc)
         : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem]: A holds two bf16 per 32-bit column, K along the columns
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi_b, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(hi_b), "r"(idesc), "r"((uint32_t)acc)
         : "memory");
 }
-// Arrive on `bar` once every MMA this thread has issued is done.
+// Arrive on `bar` once every MMA issued so far is done.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                  : "memory");
@@ -79,12 +112,68 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
+// Waits for this thread's tensor-memory loads; `v` are their results, which nothing
+// may use (or copy) before.
+template <int C>
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[C][16]) {
+    tmem_ld_wait();
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(v[c][e]));
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+
+// Two fp32 lanes per instruction.
+__device__ __forceinline__ uint64_t bits2(float2 v) { return (uint64_t)__float_as_uint(v.x) | (uint64_t)__float_as_uint(v.y) << 32; }
+__device__ __forceinline__ float2 float2_of(uint64_t b) {
+    return make_float2(__uint_as_float((uint32_t)b), __uint_as_float((uint32_t)(b >> 32)));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return float2_of(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+    return float2_of(d);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Three-way maximum that keeps a NaN.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// 2^x of two values on the FMA pipes, for x <= 2^7: x = n + f with n the nearest
+// integer, 2^f by the polynomial of degree 4 with the least relative error on
+// [-1/2, 1/2] (2.6e-6, found by exchange; probabilities keep 8 bits), and n added
+// to the exponent.  x is held at -126, whose power no sum in fp32 notices.
+__device__ __forceinline__ float2 ex2_poly(float2 x) {
+    const float kRound = 12582912.0f;                   // 1.5 * 2^23: the sum's last bits are n
+    x = make_float2(fmaxf(x.x, -126.0f), fmaxf(x.y, -126.0f));
+    const float2 t = add2(x, both(kRound));
+    const float2 f = fma2(add2(t, both(-kRound)), both(-1.0f), x);
+    float2 p = fma2(both(0.009570102207362652f), f, both(0.05591785907745361f));
+    p = fma2(p, f, both(0.240247443318367f));
+    p = fma2(p, f, both(0.6931217908859253f));
+    p = fma2(p, f, both(0.9999992847442627f));
+    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 
 // ------------------------------------------------------------- arguments
@@ -177,81 +266,128 @@ __device__ __forceinline__ void zero_rows(uint8_t *tile, int valid, int end) {
             *reinterpret_cast<uint4 *>(tile + c * CHUNK + valid * 128 + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
-// K-major operand (chunks of 64 columns, CHUNK bytes each), k-step of 16 columns.
+// Descriptors of a tile (chunks of 64 columns, CHUNK bytes each): the low word of
+// its first k-step, what the k-th step adds to it, and the high word.  K-major,
+// steps of 16 columns ...
+__device__ __forceinline__ uint32_t desc_k(uint32_t tile) { return (uint32_t)smem_desc(tile, 16, 1024, kLayoutSw128); }
 template <int CHUNK>
-__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int kstep) {
-    return smem_desc(tile + (kstep >> 2) * CHUNK + (kstep & 3) * 32, 16, 1024, kLayoutSw128);
-}
-// The same tile read along its rows (MN-major): k-step of 16 rows, N = the columns.
+__host__ __device__ constexpr uint32_t step_k(int k) { return (uint32_t)((k >> 2) * CHUNK + (k & 3) * 32) >> 4; }
+// ... or read along its rows (MN-major): steps of 16 rows, N = the columns.
 template <int CHUNK>
-__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int kstep) {
-    return smem_desc(tile + kstep * 2048, CHUNK, 1024, kLayoutSw128);
-}
+__device__ __forceinline__ uint32_t desc_mn(uint32_t tile) { return (uint32_t)smem_desc(tile, CHUNK, 1024, kLayoutSw128); }
+__host__ __device__ constexpr uint32_t step_mn(int k) { return (uint32_t)(k * 2048) >> 4; }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | ((uint32_t)kLayoutSw128 << 29);
 __host__ __device__ constexpr uint32_t idesc_b_mn(int M, int N) { return idesc_bf16_f32(M, N) | (1u << 16); }
 
 // ------------------------------------------------------------- forward
 //
 // A block takes 256 query rows of one sequence and head as two tiles of 128,
-// and streams the sequence's keys and values past them in tiles of 128.  Roles:
-// warps 0-3 and 4-7 do the softmax of tile 0 and 1 (one thread per row: row
-// maximum and sum need no shuffles), warp 8 loads, warp 9 issues the MMAs.
-// While one tile's softmax runs, the tensor cores work for the other.  Scores
-// (fp32) and probabilities (bf16, in the same columns) stay in tensor memory;
-// the output accumulates there too and is rescaled only when a row's maximum
-// has grown by more than 2^8, which keeps P in bf16's range and is rare.
+// and streams the sequence's keys and values past them.  Roles: warps 0-3 and
+// 4-7 do the softmax of tile 0 and 1 (one thread per row: row maximum and sum
+// need no shuffles), warp 8 loads, warp 9 issues the MMAs.  Scores (fp32) and
+// probabilities (bf16) have columns of their own in tensor memory, so the scores
+// of tile j + 1 are made while j's exponentials are, and the softmax never waits
+// for a product.  The output accumulates in tensor memory too and is rescaled
+// only when a row's maximum has grown by more than 2^8, which keeps P in bf16's
+// range and is rare.
 
-constexpr int kFwdThreads = 320;
-constexpr int kFwdStages = 4;
+constexpr int kFwdThreads = 384;              // 168 registers each = 256 * 224 + 128 * 56
+constexpr int kPolyOf4 = 1;                     // of four pairs of exponentials, how many the FMA pipes take
 
 template <int DP>
 constexpr int kChunks = DP > 64 ? 2 : 1;
 
+// Keys per tile: two tiles' scores, probabilities (half as wide) and outputs
+// share the 512 columns of tensor memory, 3 KT + 2 DP <= 512.
 template <int DP>
-constexpr size_t kFwdSmem = (size_t)(2 + kFwdStages) * kChunks<DP> * kChunkBytes + 1024 + 256;
+constexpr int kKeys = DP <= 64 ? 128 : (DP <= 80 ? 112 : (DP <= 96 ? 96 : 80));
+
+template <int DP>
+struct FwdShape {
+    static constexpr int kC = kChunks<DP>, KT = kKeys<DP>;
+    static constexpr int kChunk = KT * 128;                    // bytes of KT rows of 64 bf16
+    static constexpr uint32_t kQ = kC * kChunkBytes, kKv = kC * kChunk;
+    static constexpr int kStages = DP <= 64 ? 8 : 5;
+    static constexpr size_t kSmem = 2 * kQ + (size_t)kStages * kKv + 1024;
+    static constexpr uint32_t kColS = 0, kColP = 2 * KT, kColO = 3 * KT;
+    static_assert(3 * KT + 2 * DP <= 512 && kSmem + 1024 <= 232448 && KT % 16 == 0, "on-chip memory");
+};
 
 struct FwdBars {
-    uint64_t full[kFwdStages], empty[kFwdStages], tail, qfull, s_full[2], p_full[2], o_full[2], drain;
+    uint64_t full[8], empty[8], tail, qfull, s_full[2], s_free[2], p_full[2], pv_done[2], drain[2], turn[2][4];
     uint32_t tmem;
     int abort;
     Work w;
 };
 
+// p = 2^(s sl2 - base) of one row of 16 C scores, as bf16 pairs; returns the row's
+// sum.  Of four pairs POLY go to the FMA pipes: the special-function unit gives
+// 16 results a clock and would bound the kernel alone.
+template <int POLY, int C>
+__device__ __forceinline__ float exp_row(const uint32_t (&s)[C][16], float sl2, float base, uint32_t (&pk)[C][8]) {
+    float2 sum[2] = {both(0.f), both(0.f)};
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float2 x = fma2(make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])), both(sl2),
+                                  both(-base));
+            const float2 r = (e & 3) < POLY ? ex2_poly(x) : make_float2(ex2(x.x), ex2(x.y));
+            sum[e & 1] = add2(sum[e & 1], r);
+            pk[c][e] = pack_bf16x2(r.x, r.y);
+        }
+    const float2 t = add2(sum[0], sum[1]);
+    return t.x + t.y;
+}
+
 // Online softmax of one 128-row tile; all 128 threads of its warps.
 template <int DP>
-__device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, const Work &w, int tile, int n_kv, int h) {
+__device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, const Work &w, int tile, int n_kv, int n_other, int h) {
+    using S = FwdShape<DP>;
+    constexpr int C = S::KT / 16;
     volatile int *abort = &B.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // 32 lanes a warp, in bits 16..
-    const uint32_t ts = B.tmem + lanes + tile * 128, to = B.tmem + lanes + 256 + tile * 128;
-    const int i = w.row + tile * kTile + (warp & 3) * 32 + lane;  // row within the sequence
+    const uint32_t lanes = B.tmem + ((uint32_t)(warp & 3) << 21);  // 32 lanes a warp, in bits 16..
+    const uint32_t ts = lanes + S::kColS + tile * S::KT, tp = lanes + S::kColP + tile * (S::KT / 2);
+    const uint32_t to = lanes + S::kColO + tile * DP;
+    const int i = w.row + tile * kTile + (warp & 3) * 32 + lane;   // row within the sequence
     const int limit = keys_seen(P, w, i);
     const float sl2 = P.scale * kLog2e;
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n_kv; ++j) {
         if (!warp_wait(&B.s_full[tile], j & 1, abort)) return;
         tc_fence_after();
-        uint32_t s[4][32];
+        uint32_t s[C][16];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + 32 * c, s[c]);
-        tmem_ld_wait();
-        if (__any_sync(0xffffffffu, (j + 1) * kTile > limit)) {
+        for (int c = 0; c < C; ++c) tmem_ld_x16(ts + 16 * c, s[c]);
+        tmem_ld_wait_for(s);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&B.s_free[tile]));
+        const bool cut = __any_sync(0xffffffffu, (j + 1) * S::KT > limit);
+        if (cut) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < C; ++c)
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (j * kTile + 32 * c + e >= limit) s[c][e] = __float_as_uint(-INFINITY);
+                for (int e = 0; e < 16; ++e)
+                    if (j * S::KT + 16 * c + e >= limit) s[c][e] = __float_as_uint(-INFINITY);
         }
-        float mx = m;
+        float mx4[4] = {m, m, m, m};
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(s[c][e]));
+            for (int e = 0; e < 16; e += 8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mx4[k] = max3_nan(mx4[k], __uint_as_float(s[c][e + 2 * k]), __uint_as_float(s[c][e + 2 * k + 1]));
+        const float mx = max3_nan(max3_nan(mx4[0], mx4[1], mx4[2]), mx4[3], mx4[3]);
         if (__any_sync(0xffffffffu, (mx - m) * sl2 > 8.0f)) {
-            // MMAs complete in order: S(j) is there, so P V of j - 1 is done
             const float f = m == -INFINITY ? 0.f : ex2((m - mx) * sl2);
             l *= f;
             m = mx;
             if (j > 0) {
+                if (!warp_wait(&B.pv_done[tile], (j - 1) & 1, abort)) return;
+                tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < DP / 16; ++c) {
                     uint32_t o[16];
@@ -263,29 +399,28 @@ __device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, con
                 }
             }
         }
-        const float base = m == -INFINITY ? 0.f : m * sl2;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float a = ex2(fmaf(__uint_as_float(s[c][2 * e]), sl2, -base));
-                const float b = ex2(fmaf(__uint_as_float(s[c][2 * e + 1]), sl2, -base));
-                sum[e & 1] += a;
-                sum[2 + (e & 1)] += b;
-                pk[e] = pack_bf16x2(a, b);
-            }
-            tmem_st_x16(ts + 16 * c, pk);
+        // a NaN or +inf score makes the row NaN, as the formula does; a row that has seen no key stays at 0
+        const float base = mx == -INFINITY ? 0.f : fmaf(m, sl2, mx - mx);
+        // the two warps of an SM quarter take turns at the exponentials (tile 0 first):
+        // while one fills the special-function unit, the other waits, loads and stores
+        const int turn = tile ? j : j - 1;
+        if (turn >= 0 && turn < n_other && !warp_wait(&B.turn[tile][warp & 3], turn & 1, abort)) return;
+        uint32_t pk[C][8];
+        l += cut ? exp_row<0, C>(s, sl2, base, pk) : exp_row<kPolyOf4, C>(s, sl2, base, pk);
+        if (lane == 0) mbar_arrive(smem_addr(&B.turn[1 - tile][warp & 3]));
+        if (j > 0) {                                               // P V of j - 1 has read its P
+            if (!warp_wait(&B.pv_done[tile], (j - 1) & 1, abort)) return;
+            tc_fence_after();
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+        for (int c = 0; c < C; ++c) tmem_st_x8(tp + 8 * c, pk[c]);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&B.p_full[tile]));
     }
     if (n_kv > 0) {
-        if (!warp_wait(&B.o_full[tile], 0, abort)) return;
+        if (!warp_wait(&B.pv_done[tile], (n_kv - 1) & 1, abort)) return;
         tc_fence_after();
     }
     const bool mine = i < w.lq;
@@ -313,17 +448,149 @@ __device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, con
         P.lse[(int64_t)h * P.Nq + w.q0 + i] = limit > 0 ? m * P.scale + logf(l) : -INFINITY;
 }
 
+// Loads (one warp): Q, then K0 K1 V0 K2 V1 ... (the order of use) through one ring.
+template <int DP>
+__device__ __forceinline__ void fwd_load(const AttnParams &P, FwdBars &B, const Work &w, const CUtensorMap &mq,
+                                         const CUtensorMap &mk, const CUtensorMap &mv, uint8_t *sq, uint8_t *ring, bool two,
+                                         int n_max, int h, int hk) {
+    using S = FwdShape<DP>;
+    constexpr int KT = S::KT;
+    volatile int *abort = &B.abort;
+    const int lane = threadIdx.x & 31;
+    if (n_max > 0 && lane == 0) {
+        mbar_arrive_expect_tx(smem_addr(&B.qfull), (two ? 2 : 1) * S::kQ);
+        for (int t = 0; t < (two ? 2 : 1); ++t)
+            for (int c = 0; c < S::kC; ++c)
+                tma_load_3d(smem_addr(sq + t * S::kQ + c * kChunkBytes), &mq, smem_addr(&B.qfull), 64 * c, h,
+                            w.q0 + w.row + t * kTile);
+    }
+    int f = 0;
+    bool ok = true;
+    for (; f < 2 * n_max; ++f) {
+        const int slot = f % S::kStages;
+        const bool is_v = f == 2 * n_max - 1 || (f > 0 && !(f & 1));
+        const int j = f == 2 * n_max - 1 ? n_max - 1 : (is_v ? (f >> 1) - 1 : (f + 1) >> 1);
+        ok = warp_wait(&B.empty[slot], ((f / S::kStages) & 1) ^ 1, abort);
+        if (!ok) break;
+        uint8_t *dst = ring + slot * S::kKv;
+        const int valid = min(w.lk - j * KT, KT);
+        const bool clean = is_v && valid < KT;          // the last tile of V: zeros behind the sequence
+        uint64_t *bar = clean ? &B.tail : &B.full[slot];
+        if (lane == 0) {
+            mbar_arrive_expect_tx(smem_addr(bar), S::kKv);
+            for (int c = 0; c < S::kC; ++c)
+                tma_load_3d(smem_addr(dst + c * S::kChunk), is_v ? &mv : &mk, smem_addr(bar), 64 * c, hk,
+                            w.k0 + j * KT);
+        }
+        __syncwarp();
+        if (clean) {
+            ok = warp_wait(&B.tail, 0, abort);
+            if (!ok) {
+                int never = 0;
+                block_wait(&B.tail, 0, &never);
+                break;
+            }
+            zero_rows<S::kC, S::kChunk>(dst, valid, (valid + 15) & ~15);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&B.full[slot]));
+        }
+    }
+    if (!ok) {   // a wait gave up: the copies in flight still land before the block ends
+        int never = 0;
+        block_wait(&B.qfull, 0, &never);
+        for (int s = max(f - S::kStages, 0); s < f; ++s)
+            block_wait(&B.full[s % S::kStages], (s / S::kStages) & 1, &never);
+    }
+}
+
+// MMAs of one query tile (one warp): S of the next keys as soon as the softmax has
+// read the last, P V when P is there.  Each tile has a warp of its own: the issuing
+// warp shares its instruction queue with the exponentials, and one warp for both
+// tiles spent longer queueing than the tensor cores working.
+template <int DP>
+__device__ __forceinline__ void fwd_mma(FwdBars &B, const Work &w, uint8_t *sq, uint8_t *ring, int t, int n, int n_max) {
+    using S = FwdShape<DP>;
+    constexpr int KT = S::KT;
+    constexpr uint32_t kIdS = idesc_bf16_f32(kTile, KT), kIdO = idesc_b_mn(kTile, DP);
+    volatile int *abort = &B.abort;
+    const uint32_t one = elect_one(), tm = B.tmem;
+    const uint32_t d_q = desc_k(smem_addr(sq)) + t * (S::kQ >> 4), d_k = desc_k(smem_addr(ring));
+    const uint32_t d_v = desc_mn<S::kChunk>(smem_addr(ring));
+    const uint32_t ts = tm + S::kColS + t * KT, tp = tm + S::kColP + t * (KT / 2), to = tm + S::kColO + t * DP;
+    auto slot_of = [](int f) { return (uint32_t)(f % S::kStages) * (S::kKv >> 4); };
+    auto wait_full = [&](int f) { return warp_wait(&B.full[f % S::kStages], (f / S::kStages) & 1, abort); };
+    auto issue_s = [&](int f) {
+        const uint32_t b = d_k + slot_of(f);
+        if (one) {
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+                mma_ss(ts, d_q + step_k<kChunkBytes>(k), b + step_k<S::kChunk>(k), kDescHi, kDescHi, kIdS, k > 0);
+            mma_commit(&B.s_full[t]);
+            mma_commit(&B.empty[f % S::kStages]);
+        }
+        __syncwarp();
+    };
+    // a tile that needs none of the keys at f gives the slot back at once
+    auto skip = [&](int f) {
+        if (one) mbar_arrive(smem_addr(&B.empty[f % S::kStages]));
+        __syncwarp();
+    };
+    bool ok = n_max == 0 || (warp_wait(&B.qfull, 0, abort) && wait_full(0));
+    if (ok && n_max > 0) {
+        tc_fence_after();
+        if (n > 0) issue_s(0);
+        else skip(0);
+    }
+    for (int j = 0; j < n_max && ok; ++j) {
+        const bool more = j + 1 < n_max;
+        const int fk = 2 * j + 1, fv = more ? 2 * j + 2 : 2 * j + 1;
+        if (more) {                                         // the next scores, once the last have been read
+            ok = wait_full(fk) && (j + 1 >= n || warp_wait(&B.s_free[t], j & 1, abort));
+            if (!ok) break;
+            tc_fence_after();
+            if (j + 1 < n) issue_s(fk);
+            else skip(fk);
+        }
+        ok = wait_full(fv) && (j >= n || warp_wait(&B.p_full[t], j & 1, abort));
+        if (!ok) break;
+        tc_fence_after();
+        if (j < n) {
+            const int steps = (min(w.lk - j * KT, KT) + 15) / 16;
+            const uint32_t b = d_v + slot_of(fv);
+            if (one) {
+                mma_ts(to, tp, b, kDescHi, kIdO, j > 0);
+                if (steps == KT / 16) {
+#pragma unroll
+                    for (int k = 1; k < KT / 16; ++k) mma_ts(to, tp + 8 * k, b + step_mn(k), kDescHi, kIdO, true);
+                } else {
+                    for (int k = 1; k < steps; ++k) mma_ts(to, tp + 8 * k, b + step_mn(k), kDescHi, kIdO, true);
+                }
+                mma_commit(&B.pv_done[t]);
+                mma_commit(&B.empty[fv % S::kStages]);
+            }
+            __syncwarp();
+        } else {
+            skip(fv);
+        }
+    }
+    if (!ok) {   // MMAs in flight finish before their tensor memory is freed
+        int never = 0;
+        if (one) mma_commit(&B.drain[t]);
+        warp_wait(&B.drain[t], 0, &never);
+    }
+}
+
+// mk, mv: boxes of kKeys rows; mq: of 128.
 template <int DP>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ AttnParams P) {
-    constexpr int kC = kChunks<DP>;
-    constexpr uint32_t kTileBytes = kC * kChunkBytes;
+    using S = FwdShape<DP>;
+    constexpr int KT = S::KT;
     extern __shared__ uint8_t raw[];
     __shared__ FwdBars B;
-    uint8_t *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
-    uint8_t *sq = smem, *ring = smem + 2 * kTileBytes;
-    volatile int *abort = &B.abort;
+    uint8_t *sq = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023), *ring = sq + 2 * S::kQ;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.y, hk = h / (P.Hq / P.Hkv);
     if (warp == 9) {
@@ -331,14 +598,17 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         if (lane == 0) {
             B.w = w;
             B.abort = 0;
-            for (int i = 0; i < kFwdStages; ++i) mbar_init(smem_addr(&B.full[i]), 1), mbar_init(smem_addr(&B.empty[i]), 1);
+            const int tiles = w.lq - w.row > kTile ? 2 : 1;  // each gives a slot back
+            for (int i = 0; i < S::kStages; ++i) mbar_init(smem_addr(&B.full[i]), 1), mbar_init(smem_addr(&B.empty[i]), tiles);
             mbar_init(smem_addr(&B.tail), 1);
             mbar_init(smem_addr(&B.qfull), 1);
-            mbar_init(smem_addr(&B.drain), 1);
             for (int t = 0; t < 2; ++t) {
+                mbar_init(smem_addr(&B.drain[t]), 1);
+                for (int u = 0; u < 4; ++u) mbar_init(smem_addr(&B.turn[t][u]), 1);
                 mbar_init(smem_addr(&B.s_full[t]), 1);
+                mbar_init(smem_addr(&B.s_free[t]), 4);
                 mbar_init(smem_addr(&B.p_full[t]), 4);
-                mbar_init(smem_addr(&B.o_full[t]), 1);
+                mbar_init(smem_addr(&B.pv_done[t]), 1);
             }
             fence_mbar_init();
             prefetch_tmap(&mq);
@@ -356,112 +626,20 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const int n_tiles = w.lq - w.row > kTile ? 2 : 1;
-    int n_kv[2];                                            // key tiles that each query tile meets
-    for (int t = 0; t < 2; ++t) {
+    // key tiles that each query tile meets (the second tile may be missing)
+    auto tiles_of = [&](int t) {
         const int last = min(w.row + (t + 1) * kTile, w.lq) - 1;
-        n_kv[t] = t < n_tiles ? (keys_seen(P, w, last) + kTile - 1) / kTile : 0;
-    }
-    const int n_max = max(n_kv[0], n_kv[1]);
-    if (warp < 4) {
-        fwd_softmax<DP>(P, B, w, 0, n_kv[0], h);
-    } else if (warp < 8) {
-        if (n_tiles > 1) fwd_softmax<DP>(P, B, w, 1, n_kv[1], h);
-    } else if (warp == 8) {
-        // ---- loads: Q, then K0 V0 K1 V1 ... through one ring
-        if (n_max > 0 && lane == 0) {
-            mbar_arrive_expect_tx(smem_addr(&B.qfull), n_tiles * kTileBytes);
-            for (int t = 0; t < n_tiles; ++t)
-                for (int c = 0; c < kC; ++c)
-                    tma_load_3d(smem_addr(sq + t * kTileBytes + c * kChunkBytes), &mq, smem_addr(&B.qfull), 64 * c, h,
-                                w.q0 + w.row + t * kTile);
-        }
-        int f = 0;
-        bool ok = true;
-        for (; f < 2 * n_max && ok; ++f) {
-            const int slot = f % kFwdStages, j = f >> 1;
-            const bool is_v = f & 1;
-            ok = warp_wait(&B.empty[slot], ((f / kFwdStages) & 1) ^ 1, abort);
-            if (!ok) break;
-            uint8_t *dst = ring + slot * kTileBytes;
-            const int valid = min(w.lk - j * kTile, kTile);
-            const bool clean = is_v && valid < kTile;       // the last tile of V: zeros behind the sequence
-            uint64_t *bar = clean ? &B.tail : &B.full[slot];
-            if (lane == 0) {
-                mbar_arrive_expect_tx(smem_addr(bar), kTileBytes);
-                for (int c = 0; c < kC; ++c)
-                    tma_load_3d(smem_addr(dst + c * kChunkBytes), is_v ? &mv : &mk, smem_addr(bar), 64 * c, hk,
-                                w.k0 + j * kTile);
-            }
-            __syncwarp();
-            if (clean) {
-                ok = warp_wait(&B.tail, 0, abort);
-                if (!ok) {
-                    int never = 0;
-                    mbar_wait(smem_addr(&B.tail), 0, &never);
-                    break;
-                }
-                zero_rows<kC, kChunkBytes>(dst, valid, (valid + 15) & ~15);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&B.full[slot]));
-            }
-        }
-        if (!ok) {   // a wait gave up: the copies in flight still land before the block ends
-            int never = 0;
-            mbar_wait(smem_addr(&B.qfull), 0, &never);
-            for (int s = max(f - kFwdStages, 0); s < f; ++s) {
-                mbar_wait(smem_addr(&B.full[s % kFwdStages]), (s / kFwdStages) & 1, &never);
-            }
-        }
-    } else if (lane == 0 && n_max > 0) {
-        // ---- MMAs
-        constexpr uint32_t kIdS = idesc_bf16_f32(kTile, kTile), kIdO = idesc_b_mn(kTile, DP);
-        const int ksteps = (P.D + 15) / 16;
-        const uint32_t a_q = smem_addr(sq), a_r = smem_addr(ring);
-        auto wait_full = [&](int f) {
-            return mbar_wait(smem_addr(&B.full[f % kFwdStages]), (f / kFwdStages) & 1, abort);
-        };
-        auto issue_s = [&](int t, int f) {
-            for (int k = 0; k < ksteps; ++k)
-                mma_ss(B.tmem + t * 128, desc_k<kChunkBytes>(a_q + t * kTileBytes, k),
-                       desc_k<kChunkBytes>(a_r + f % kFwdStages * kTileBytes, k), kIdS, k > 0);
-            mma_commit(&B.s_full[t]);
-        };
-        bool ok = mbar_wait(smem_addr(&B.qfull), 0, abort) && wait_full(0);
-        if (ok) {
-            tc_fence_after();
-            for (int t = 0; t < n_tiles; ++t)
-                if (n_kv[t] > 0) issue_s(t, 0);
-            mma_commit(&B.empty[0]);
-        }
-        for (int j = 0; j < n_max && ok; ++j) {
-            const int fv = 2 * j + 1, fk = 2 * j + 2;
-            const bool more = j + 1 < n_max;
-            ok = wait_full(fv) && (!more || wait_full(fk));
-            const int rows = min(w.lk - j * kTile, kTile);
-            for (int t = 0; t < n_tiles && ok; ++t) {
-                if (j < n_kv[t]) {
-                    ok = mbar_wait(smem_addr(&B.p_full[t]), j & 1, abort);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const int psteps = (rows + 15) / 16;
-                    for (int k = 0; k < psteps; ++k)
-                        mma_ts(B.tmem + 256 + t * 128, B.tmem + t * 128 + 8 * k,
-                               desc_mn<kChunkBytes>(a_r + fv % kFwdStages * kTileBytes, k), kIdO, j > 0 || k > 0);
-                    if (j + 1 == n_kv[t]) mma_commit(&B.o_full[t]);
-                }
-                if (j + 1 < n_kv[t]) issue_s(t, fk);
-            }
-            if (!ok) break;
-            mma_commit(&B.empty[fv % kFwdStages]);
-            if (more) mma_commit(&B.empty[fk % kFwdStages]);
-        }
-        if (!ok) {   // MMAs in flight finish before their tensor memory is freed
-            int never = 0;
-            mma_commit(&B.drain);
-            mbar_wait(smem_addr(&B.drain), 0, &never);
-        }
+        return w.lq - w.row > t * kTile ? (keys_seen(P, w, last) + KT - 1) / KT : 0;
+    };
+    const bool two = w.lq - w.row > kTile;
+    const int n0 = tiles_of(0), n1 = tiles_of(1), n_max = max(n0, n1);
+    if (warp < 8) {
+        regs_up<224>();
+        if (warp < 4 || two) fwd_softmax<DP>(P, B, w, warp >> 2, warp < 4 ? n0 : n1, warp < 4 ? n1 : n0, h);
+    } else {
+        regs_down<56>();
+        if (warp == 8) fwd_load<DP>(P, B, w, mq, mk, mv, sq, ring, two, n_max, h, hk);
+        else if (warp < (two ? 11 : 10)) fwd_mma<DP>(B, w, sq, ring, warp - 9, warp == 9 ? n0 : n1, n_max);
     }
     __syncwarp();
     tc_fence_before();
@@ -742,7 +920,7 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
                 ok = warp_wait(&B.tail, tails & 1, abort);
                 if (!ok) {
                     int never = 0;
-                    mbar_wait(smem_addr(&B.tail), tails & 1, &never);
+                    block_wait(&B.tail, tails & 1, &never);
                     break;
                 }
                 ++tails;
@@ -754,27 +932,43 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
         }
         if (!ok) {   // a wait gave up: the copies in flight still land before the block ends
             int never = 0;
-            mbar_wait(smem_addr(&B.xfull), 0, &never);
+            block_wait(&B.xfull, 0, &never);
             for (int s = max(f - kBwdStages, 0); s < f; ++s)
-                mbar_wait(smem_addr(&B.full[s % kBwdStages]), (s / kBwdStages) & 1, &never);
+                block_wait(&B.full[s % kBwdStages], (s / kBwdStages) & 1, &never);
         }
-    } else if (warp == 9 && lane == 0 && st.n > 0) {
+    } else if (warp == 9 && st.n > 0) {
         // ---- MMAs
         constexpr uint32_t kIdS = idesc_bf16_f32(kTile, kStream), kIdA = idesc_b_mn(kTile, DP);
-        const int ksteps = (P.D + 15) / 16;
-        const uint32_t a0 = smem_addr(kept), r0 = smem_addr(ring);
+        const uint32_t one = elect_one(), tm = B.tmem;
+        const uint32_t d_x0 = desc_k(smem_addr(kept)), d_x1 = desc_k(smem_addr(kept + kKept));
+        const uint32_t d_y0 = desc_k(smem_addr(ring)), d_y1 = desc_k(smem_addr(ring + kOne));
+        const uint32_t d_z0 = desc_mn<kStreamChunk>(smem_addr(ring)), d_z1 = desc_mn<kStreamChunk>(smem_addr(ring + kOne));
+        auto slot_of = [](int f) { return (uint32_t)(f % kBwdStages) * (2 * kOne >> 4); };
+        auto wait_full = [&](int f) { return warp_wait(&B.full[f % kBwdStages], (f / kBwdStages) & 1, abort); };
         auto issue_s = [&](int j) {
-            const uint32_t y = r0 + j % kBwdStages * 2 * kOne, d = B.tmem + (j & 1) * 128;
-            for (int k = 0; k < ksteps; ++k)
-                mma_ss(d, desc_k<kChunkBytes>(a0, k), desc_k<kStreamChunk>(y, k), kIdS, k > 0);
-            for (int k = 0; k < ksteps; ++k)
-                mma_ss(d + 64, desc_k<kChunkBytes>(a0 + kKept, k), desc_k<kStreamChunk>(y + kOne, k), kIdS, k > 0);
-            mma_commit(&B.s_full[j & 1]);
+            const uint32_t d = tm + (j & 1) * 128, y0 = d_y0 + slot_of(j), y1 = d_y1 + slot_of(j);
+            if (one) {
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    mma_ss(d, d_x0 + step_k<kChunkBytes>(k), y0 + step_k<kStreamChunk>(k), kDescHi, kDescHi, kIdS, k > 0);
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    mma_ss(d + 64, d_x1 + step_k<kChunkBytes>(k), y1 + step_k<kStreamChunk>(k), kDescHi, kDescHi, kIdS, k > 0);
+                mma_commit(&B.s_full[j & 1]);
+            }
+            __syncwarp();
         };
-        auto wait_full = [&](int f) {
-            return mbar_wait(smem_addr(&B.full[f % kBwdStages]), (f / kBwdStages) & 1, abort);
+        // kept rows += A (tensor memory) times the streamed tile at z
+        auto issue_acc = [&](uint32_t acc, uint32_t a, uint32_t z, int steps, bool add) {
+            mma_ts(acc, a, z, kDescHi, kIdA, add);
+            if (steps == kStream / 16) {
+#pragma unroll
+                for (int k = 1; k < kStream / 16; ++k) mma_ts(acc, a + 8 * k, z + step_mn(k), kDescHi, kIdA, true);
+            } else {
+                for (int k = 1; k < steps; ++k) mma_ts(acc, a + 8 * k, z + step_mn(k), kDescHi, kIdA, true);
+            }
         };
-        bool ok = mbar_wait(smem_addr(&B.xfull), 0, abort);
+        bool ok = warp_wait(&B.xfull, 0, abort);
         for (int j = 0; j < 2 && j < st.n && ok; ++j) {
             ok = wait_full(j);
             tc_fence_after();
@@ -783,17 +977,17 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
         for (int j = 0; j < st.n && ok; ++j) {
             const int b = j & 1, row = (st.first + (KEYS ? j % st.per_head : j)) * kStream;
             const int steps = (min(y_len - row, kStream) + 15) / 16;
-            const uint32_t y = r0 + j % kBwdStages * 2 * kOne, d = B.tmem + b * 128;
-            ok = mbar_wait(smem_addr(&B.d_full[b]), (j >> 1) & 1, abort);
+            const uint32_t d = tm + b * 128;
+            ok = warp_wait(&B.d_full[b], (j >> 1) & 1, abort);
             if (!ok) break;
             tc_fence_after();
-            if (KEYS)
-                for (int k = 0; k < steps; ++k)
-                    mma_ts(B.tmem + 256, d + 8 * k, desc_mn<kStreamChunk>(y + kOne, k), kIdA, j > 0 || k > 0);
-            for (int k = 0; k < steps; ++k)
-                mma_ts(B.tmem + 384, d + 64 + 8 * k, desc_mn<kStreamChunk>(y, k), kIdA, j > 0 || k > 0);
-            mma_commit(&B.empty[j % kBwdStages]);
-            if (j + 1 == st.n) mma_commit(&B.acc_full);
+            if (one) {
+                if (KEYS) issue_acc(tm + 256, d, d_z1 + slot_of(j), steps, j > 0);
+                issue_acc(tm + 384, d + 64, d_z0 + slot_of(j), steps, j > 0);
+                mma_commit(&B.empty[j % kBwdStages]);
+                if (j + 1 == st.n) mma_commit(&B.acc_full);
+            }
+            __syncwarp();
             if (j + 2 < st.n) {
                 ok = wait_full(j + 2);
                 tc_fence_after();
@@ -802,8 +996,8 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
         }
         if (!ok) {   // MMAs in flight finish before their tensor memory is freed
             int never = 0;
-            mma_commit(&B.drain);
-            mbar_wait(smem_addr(&B.drain), 0, &never);
+            if (one) mma_commit(&B.drain);
+            warp_wait(&B.drain, 0, &never);
         }
     }
     __syncwarp();

@@ -167,6 +167,16 @@ auto with_head_size(int D, F &&f) {
     return f(std::integral_constant<int, 128>());
 }
 
+// Prepares an attention kernel of 384 threads whose warpgroups divide the
+// registers anew (setmaxnreg): more than it was launched with would be waited for
+// without end, so a build that gave it fewer is refused.
+template <class Kernel>
+bool ready_to_launch(Kernel kern, size_t smem) {
+    cudaFuncAttributes at;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess &&
+           cudaFuncGetAttributes(&at, kern) == cudaSuccess && at.numRegs * kFwdThreads >= 256 * 224 + 128 * 56;
+}
+
 // Tiles of `rows` rows that n rows in n_seq sequences can make, at most.
 unsigned max_tiles(int64_t n, int n_seq, int rows) { return (unsigned)(n / rows + std::min<int64_t>(n_seq, n)); }
 
@@ -437,19 +447,17 @@ pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, 
     P.k = heads_ptr(k, Nk, a->Hkv);
     P.v = heads_ptr(v, Nk, a->Hkv);
     P.lse = lse;
-    // without keys their maps are not read
-    CUtensorMap mq, mk, mv;
-    if (!make_heads_tmap(&mq, q, Nq, a->Hq, D, kTile)) return PE_ERR_CUDA;
-    mk = mv = mq;
-    if (Nk > 0 && (!make_heads_tmap(&mk, k, Nk, a->Hkv, D, kTile) || !make_heads_tmap(&mv, v, Nk, a->Hkv, D, kTile)))
-        return PE_ERR_CUDA;
-    const dim3 grid(max_tiles(Nq, n_seq, 2 * kTile), (unsigned)a->Hq);
     return with_head_size(D, [&](auto dp) {
-        constexpr int DP = decltype(dp)::value;
-        auto kern = pe_attn_fwd_kernel<DP>;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFwdSmem<DP>) != cudaSuccess)
+        using S = FwdShape<decltype(dp)::value>;
+        CUtensorMap mq, mk, mv;
+        if (!make_heads_tmap(&mq, q, Nq, a->Hq, D, kTile)) return PE_ERR_CUDA;
+        mk = mv = mq;                                       // without keys their maps are not read
+        if (Nk > 0 && (!make_heads_tmap(&mk, k, Nk, a->Hkv, D, S::KT) || !make_heads_tmap(&mv, v, Nk, a->Hkv, D, S::KT)))
             return PE_ERR_CUDA;
-        kern<<<grid, kFwdThreads, kFwdSmem<DP>, (cudaStream_t)stream>>>(mq, mk, mv, P);
+        auto kern = pe_attn_fwd_kernel<decltype(dp)::value>;
+        if (!ready_to_launch(kern, S::kSmem)) return PE_ERR_CUDA;
+        const dim3 grid(max_tiles(Nq, n_seq, 2 * kTile), (unsigned)a->Hq);
+        kern<<<grid, kFwdThreads, S::kSmem, (cudaStream_t)stream>>>(mq, mk, mv, P);
         return finish(cudaGetLastError());
     });
 }
