@@ -150,6 +150,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
     return float2_of(d);
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+    return float2_of(d);
+}
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // Three-way maximum that keeps a NaN.
@@ -190,7 +195,7 @@ struct AttnParams {
     float scale;
     HeadsPtr q, k, v, out, dout, dq, dk, dv;
     float *lse;                   // [Hq, Nq]
-    float *lse2, *delta;          // [Hq, Nq]: lse * log2(e), and dout . out (backward)
+    float *nlse2, *ndelta;        // [Hq, Nq]: -lse * log2(e), and -dout . out (backward)
     int *err;
 };
 
@@ -291,7 +296,7 @@ __host__ __device__ constexpr uint32_t idesc_b_mn(int M, int N) { return idesc_b
 // only when a row's maximum has grown by more than 2^8, which keeps P in bf16's
 // range and is rare.
 
-constexpr int kFwdThreads = 384;              // 168 registers each = 256 * 224 + 128 * 56
+constexpr int kAttnThreads = 384;             // 168 registers each = 256 * 224 + 128 * 56
 constexpr int kPolyOf4 = 1;                     // of four pairs of exponentials, how many the FMA pipes take
 
 template <int DP>
@@ -319,6 +324,14 @@ struct FwdBars {
     int abort;
     Work w;
 };
+
+// MMAs in flight finish before their tensor memory is freed.
+__device__ __forceinline__ void drain_mmas(uint32_t one, uint64_t *bar) {
+    int never = 0;
+    if (one) mma_commit(bar);
+    __syncwarp();
+    warp_wait(bar, 0, &never);
+}
 
 // p = 2^(s sl2 - base) of one row of 16 C scores, as bf16 pairs; returns the row's
 // sum.  Of four pairs POLY go to the FMA pipes: the special-function unit gives
@@ -574,16 +587,12 @@ __device__ __forceinline__ void fwd_mma(FwdBars &B, const Work &w, uint8_t *sq, 
             skip(fv);
         }
     }
-    if (!ok) {   // MMAs in flight finish before their tensor memory is freed
-        int never = 0;
-        if (one) mma_commit(&B.drain[t]);
-        warp_wait(&B.drain[t], 0, &never);
-    }
+    if (!ok) drain_mmas(one, &B.drain[t]);
 }
 
 // mk, mv: boxes of kKeys rows; mq: of 128.
 template <int DP>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+__global__ void __launch_bounds__(kAttnThreads, 1)
 pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ AttnParams P) {
     using S = FwdShape<DP>;
@@ -665,22 +674,23 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
 // The streamed tiles hold 64 rows, so that two pairs (s, dp) fit in tensor
 // memory beside the sums: warps 0-3 work on one while the tensor cores fill the
 // other for warps 4-7.  p and ds go back to tensor memory as bf16 and are the A
-// operands of the sums.
+// operands of the sums.  Scores and sums are issued by a warp each, as the
+// forward pass's tiles are.  For queries ds has columns of its own, so that the
+// next scores need not wait for the sums; for keys the two sums leave no room.
 
 constexpr int kStream = 64;                       // streamed rows per tile
 constexpr int kStreamChunk = kStream * 128;       // bytes of 64 rows of 64 bf16
-constexpr int kBwdThreads = 320;
 constexpr int kBwdStages = 4;
 
 template <int DP>
 constexpr size_t kBwdSmem = (size_t)kChunks<DP> * (2 * kChunkBytes + kBwdStages * 2 * kStreamChunk) + 1024;
 
 struct BwdBars {
-    uint64_t full[kBwdStages], empty[kBwdStages], tail, xfull, s_full[2], d_full[2], acc_full, drain;
+    uint64_t full[kBwdStages], empty[kBwdStages], tail, xfull, s_full[2], s_free[2], d_full[2], acc_done[2], acc_full, drain[2];
     uint32_t tmem;
     int abort;
     Work w;
-    alignas(16) float stat[kBwdStages][2][kStream];   // lse2 and delta of the streamed queries
+    alignas(16) float stat[kBwdStages][2][kStream];   // nlse2 and ndelta of the streamed queries
 };
 
 // 4 bytes to shared memory without waiting; zero when !take.
@@ -713,18 +723,24 @@ __device__ __forceinline__ Stream stream_of(const AttnParams &P, const Work &w) 
     return st;
 }
 
+template <bool KEYS>
+struct BwdCols {                                  // of buffer b: s at b * kBuf, dp 64 behind it, ds (and p in place of s)
+    static constexpr uint32_t kBuf = KEYS ? 128 : 160, kDs = KEYS ? 64 : 128, kAcc0 = 256, kAcc1 = 384;
+};
+
 // p and ds of every second streamed tile, then half of the results; the 128
 // threads of group g, one kept row each.
 template <int DP, bool KEYS>
 __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const Work &w, const Stream &st, int g, int h) {
+    using T = BwdCols<KEYS>;
     volatile int *abort = &B.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t ts = B.tmem + lanes + g * 128, td = ts + 64;
+    const uint32_t lanes = B.tmem + ((uint32_t)(warp & 3) << 21);
+    const uint32_t ts = lanes + g * T::kBuf, td = ts + T::kDs;
     const int i = w.row + (warp & 3) * 32 + lane;           // kept row within the sequence
     const bool mine = i < (KEYS ? w.lk : w.lq);
-    const float sl2 = P.scale * kLog2e;
-    float lse2 = 0.f, delta = 0.f;
+    const float2 sl2 = both(P.scale * kLog2e);
+    float nlse2 = 0.f, ndelta = 0.f;
     int limit = 0;
     if (!KEYS) {
         limit = mine ? keys_seen(P, w, i) : 0;
@@ -736,13 +752,13 @@ __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const
                 const uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    delta += bf16lo_to_f32(x[k]) * bf16lo_to_f32(y[k]) + bf16hi_to_f32(x[k]) * bf16hi_to_f32(y[k]);
+                    ndelta -= bf16lo_to_f32(x[k]) * bf16lo_to_f32(y[k]) + bf16hi_to_f32(x[k]) * bf16hi_to_f32(y[k]);
             }
             // a row that sees no key has lse = -inf; +inf gives it p = 0 for every key
-            lse2 = limit > 0 ? P.lse[at] * kLog2e : INFINITY;
+            nlse2 = limit > 0 ? -P.lse[at] * kLog2e : -INFINITY;
             if (g == 0) {
-                P.lse2[at] = lse2;
-                P.delta[at] = delta;
+                P.nlse2[at] = nlse2;
+                P.ndelta[at] = ndelta;
             }
         }
     }
@@ -753,43 +769,56 @@ __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const
         if (!warp_wait(&B.s_full[g], n & 1, abort)) return;
         tc_fence_after();
         const int y = (st.first + (KEYS ? j % st.per_head : j)) * kStream;      // first streamed row
-        uint32_t s[2][32], d[2][32];
+        uint32_t s[4][16], d[4][16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            tmem_ld_32x32b_x32(ts + 32 * c, s[c]);
-            tmem_ld_32x32b_x32(td + 32 * c, d[c]);
+        for (int c = 0; c < 4; ++c) {
+            tmem_ld_x16(ts + 16 * c, s[c]);
+            tmem_ld_x16(ts + 64 + 16 * c, d[c]);
         }
-        tmem_ld_wait();
+        tmem_ld_wait_for(s);
+        tmem_ld_wait_for(d);
+        if (!KEYS) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&B.s_free[g]));
+        }
         // queries a key row sees start at i - shift; keys a query row sees end at limit
         const bool cut = __any_sync(0xffffffffu, KEYS ? P.causal && y < i - shift : y + kStream > limit);
+        uint32_t pp[4][8], pd[4][8];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            uint32_t pp[16], pd[16];
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-                float4 L = make_float4(lse2, lse2, lse2, lse2), T = make_float4(delta, delta, delta, delta);
+            for (int e = 0; e < 16; e += 4) {
+                float4 L = make_float4(nlse2, nlse2, nlse2, nlse2), D = make_float4(ndelta, ndelta, ndelta, ndelta);
                 if (KEYS) {
-                    L = *reinterpret_cast<const float4 *>(&B.stat[stage][0][32 * c + e]);
-                    T = *reinterpret_cast<const float4 *>(&B.stat[stage][1][32 * c + e]);
+                    L = *reinterpret_cast<const float4 *>(&B.stat[stage][0][16 * c + e]);
+                    D = *reinterpret_cast<const float4 *>(&B.stat[stage][1][16 * c + e]);
                 }
-                const float l4[4] = {L.x, L.y, L.z, L.w}, t4[4] = {T.x, T.y, T.z, T.w};
-                float p[4], q[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    p[k] = ex2(fmaf(__uint_as_float(s[c][e + k]), sl2, -l4[k]));
-                    q[k] = p[k] * (__uint_as_float(d[c][e + k]) - t4[k]);
+                for (int k = 0; k < 2; ++k) {
+                    const int at = e + 2 * k;
+                    const float2 x = fma2(make_float2(__uint_as_float(s[c][at]), __uint_as_float(s[c][at + 1])), sl2,
+                                          k ? make_float2(L.z, L.w) : make_float2(L.x, L.y));
+                    float2 p = make_float2(ex2(x.x), ex2(x.y));
+                    float2 q = mul2(p, add2(make_float2(__uint_as_float(d[c][at]), __uint_as_float(d[c][at + 1])),
+                                            k ? make_float2(D.z, D.w) : make_float2(D.x, D.y)));
                     if (cut) {
-                        const int col = y + 32 * c + e + k;
-                        if (KEYS ? col < i - shift : col >= limit) p[k] = q[k] = 0.f;
+                        const int col = y + 16 * c + at;
+                        if (KEYS ? col < i - shift : col >= limit) p.x = q.x = 0.f;
+                        if (KEYS ? col + 1 < i - shift : col + 1 >= limit) p.y = q.y = 0.f;
                     }
+                    if (KEYS) pp[c][at / 2] = pack_bf16x2(p.x, p.y);
+                    pd[c][at / 2] = pack_bf16x2(q.x, q.y);
                 }
-                pp[e / 2] = pack_bf16x2(p[0], p[1]);
-                pp[e / 2 + 1] = pack_bf16x2(p[2], p[3]);
-                pd[e / 2] = pack_bf16x2(q[0], q[1]);
-                pd[e / 2 + 1] = pack_bf16x2(q[2], q[3]);
             }
-            if (KEYS) tmem_st_x16(ts + 16 * c, pp);
-            tmem_st_x16(td + 16 * c, pd);
+        if (!KEYS && n > 0) {                               // the sums have read the last ds
+            if (!warp_wait(&B.acc_done[g], (n - 1) & 1, abort)) return;
+            tc_fence_after();
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (KEYS) tmem_st_x8(ts + 8 * c, pp[c]);
+            tmem_st_x8(td + 8 * c, pd[c]);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -802,42 +831,180 @@ __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const
     }
     // keys: group 0 writes dv, group 1 dk; queries: every second 16 columns of dq
     const bool is_dv = KEYS && g == 0;
-    const uint32_t acc = B.tmem + lanes + (is_dv ? 256 : 384);
+    const uint32_t acc = lanes + (is_dv ? T::kAcc0 : T::kAcc1);
     const float f = is_dv ? 1.0f : P.scale;
     __nv_bfloat16 *out = KEYS ? (is_dv ? P.dv : P.dk).at(w.k0 + i, h) : P.dq.at(w.q0 + i, h);
 #pragma unroll
     for (int c = 0; c < DP / 16; ++c) {
         if (!KEYS && (c & 1) != g) continue;
-        uint32_t o[16] = {0};
+        uint32_t o[1][16] = {{0}};
         if (st.n > 0) {
-            tmem_ld_x16(acc + 16 * c, o);
-            tmem_ld_wait();
+            tmem_ld_x16(acc + 16 * c, o[0]);
+            tmem_ld_wait_for(o);
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             uint32_t pk[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                pk[e] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * e]) * f, __uint_as_float(o[8 * q + 2 * e + 1]) * f);
+                pk[e] = pack_bf16x2(__uint_as_float(o[0][8 * q + 2 * e]) * f, __uint_as_float(o[0][8 * q + 2 * e + 1]) * f);
             if (mine && 16 * c + 8 * q < P.D) st_global_v4(out + 16 * c + 8 * q, pk[0], pk[1], pk[2], pk[3]);
         }
     }
 }
 
+// Loads (one warp): the kept tiles, then the streamed ones through the ring.
+template <int DP, bool KEYS>
+__device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const Work &w, const Stream &st,
+                                         const CUtensorMap &mx0, const CUtensorMap &mx1, const CUtensorMap &my0,
+                                         const CUtensorMap &my1, uint8_t *kept, uint8_t *ring, int h) {
+    constexpr int kC = kChunks<DP>;
+    constexpr uint32_t kKept = kC * kChunkBytes, kOne = kC * kStreamChunk;     // bytes of one kept / streamed tile
+    volatile int *abort = &B.abort;
+    const int lane = threadIdx.x & 31, share = P.Hq / P.Hkv;
+    const int y_len = KEYS ? w.lq : w.lk;                   // streamed rows of the sequence
+    const int x_row = (KEYS ? w.k0 : w.q0) + w.row;
+    if (lane == 0) {
+        mbar_arrive_expect_tx(smem_addr(&B.xfull), 2 * kKept);
+        for (int t = 0; t < 2; ++t)
+            for (int c = 0; c < kC; ++c)
+                for (int half = 0; half < 2; ++half)
+                    tma_load_3d(smem_addr(kept + t * kKept + c * kChunkBytes + half * kStreamChunk), t ? &mx1 : &mx0,
+                                smem_addr(&B.xfull), 64 * c, h, x_row + half * kStream);
+    }
+    int f = 0, tails = 0;
+    bool ok = true;
+    for (; f < st.n; ++f) {
+        const int slot = f % kBwdStages;
+        ok = warp_wait(&B.empty[slot], ((f / kBwdStages) & 1) ^ 1, abort);
+        if (!ok) break;
+        const int row = (st.first + (KEYS ? f % st.per_head : f)) * kStream;
+        const int y_head = KEYS ? h * share + f / st.per_head : h / share;
+        const int y_row = (KEYS ? w.q0 : w.k0) + row;
+        const int valid = min(y_len - row, kStream);
+        uint8_t *dst = ring + slot * 2 * kOne;
+        const bool clean = valid < kStream;                 // the sequence's last tile: zeros behind it
+        uint64_t *bar = clean ? &B.tail : &B.full[slot];
+        if (KEYS) {
+            const float *src = P.nlse2 + (int64_t)y_head * P.Nq + y_row;
+            const float *srd = P.ndelta + (int64_t)y_head * P.Nq + y_row;
+#pragma unroll
+            for (int e = lane; e < kStream; e += 32) {
+                const bool in = e < valid;
+                cp_async4(smem_addr(&B.stat[slot][0][e]), in ? src + e : src, in);
+                cp_async4(smem_addr(&B.stat[slot][1][e]), in ? srd + e : srd, in);
+            }
+            cp_async_arrive(smem_addr(&B.full[slot]));
+        }
+        if (lane == 0) {
+            mbar_arrive_expect_tx(smem_addr(bar), 2 * kOne);
+            for (int t = 0; t < 2; ++t)
+                for (int c = 0; c < kC; ++c)
+                    tma_load_3d(smem_addr(dst + t * kOne + c * kStreamChunk), t ? &my1 : &my0, smem_addr(bar), 64 * c,
+                                y_head, y_row);
+        }
+        __syncwarp();
+        if (clean) {
+            ok = warp_wait(&B.tail, tails & 1, abort);
+            if (!ok) {
+                int never = 0;
+                block_wait(&B.tail, tails & 1, &never);
+                break;
+            }
+            ++tails;
+            for (int t = 0; t < 2; ++t) zero_rows<kC, kStreamChunk>(dst + t * kOne, valid, (valid + 15) & ~15);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&B.full[slot]));
+        }
+    }
+    if (!ok) {   // a wait gave up: the copies in flight still land before the block ends
+        int never = 0;
+        block_wait(&B.xfull, 0, &never);
+        for (int s = max(f - kBwdStages, 0); s < f; ++s)
+            block_wait(&B.full[s % kBwdStages], (s / kBwdStages) & 1, &never);
+    }
+}
+
+// s and dp of every streamed tile (one warp).
+template <int DP, bool KEYS>
+__device__ __forceinline__ void bwd_scores(BwdBars &B, const Stream &st, uint8_t *kept, uint8_t *ring) {
+    using T = BwdCols<KEYS>;
+    constexpr int kC = kChunks<DP>;
+    constexpr uint32_t kKept = kC * kChunkBytes, kOne = kC * kStreamChunk, kIdS = idesc_bf16_f32(kTile, kStream);
+    volatile int *abort = &B.abort;
+    const uint32_t one = elect_one(), tm = B.tmem;
+    const uint32_t x0 = desc_k(smem_addr(kept)), x1 = desc_k(smem_addr(kept + kKept));
+    bool ok = warp_wait(&B.xfull, 0, abort);
+    for (int j = 0; j < st.n && ok; ++j) {
+        const int b = j & 1, n = j >> 1, slot = j % kBwdStages;
+        ok = warp_wait(&B.full[slot], (j / kBwdStages) & 1, abort) && (n == 0 || warp_wait(&B.s_free[b], (n - 1) & 1, abort));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tm + b * T::kBuf, y0 = desc_k(smem_addr(ring + slot * 2 * kOne)), y1 = y0 + (kOne >> 4);
+        if (one) {
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+                mma_ss(d, x0 + step_k<kChunkBytes>(k), y0 + step_k<kStreamChunk>(k), kDescHi, kDescHi, kIdS, k > 0);
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+                mma_ss(d + 64, x1 + step_k<kChunkBytes>(k), y1 + step_k<kStreamChunk>(k), kDescHi, kDescHi, kIdS, k > 0);
+            mma_commit(&B.s_full[b]);
+        }
+        __syncwarp();
+    }
+    if (!ok) drain_mmas(one, &B.drain[0]);
+}
+
+// The sums over the streamed tiles (one warp).
+template <int DP, bool KEYS>
+__device__ __forceinline__ void bwd_sums(BwdBars &B, const Stream &st, uint8_t *ring, int y_len) {
+    using T = BwdCols<KEYS>;
+    constexpr uint32_t kOne = kChunks<DP> * kStreamChunk, kIdA = idesc_b_mn(kTile, DP);
+    volatile int *abort = &B.abort;
+    const uint32_t one = elect_one(), tm = B.tmem;
+    // kept rows += A (tensor memory) times the streamed tile at z
+    auto add = [&](uint32_t acc, uint32_t a, uint32_t z, int steps, bool more) {
+        mma_ts(acc, a, z, kDescHi, kIdA, more);
+        if (steps == kStream / 16) {
+#pragma unroll
+            for (int k = 1; k < kStream / 16; ++k) mma_ts(acc, a + 8 * k, z + step_mn(k), kDescHi, kIdA, true);
+        } else {
+            for (int k = 1; k < steps; ++k) mma_ts(acc, a + 8 * k, z + step_mn(k), kDescHi, kIdA, true);
+        }
+    };
+    bool ok = true;
+    for (int j = 0; j < st.n && ok; ++j) {
+        const int b = j & 1, slot = j % kBwdStages, row = (st.first + (KEYS ? j % st.per_head : j)) * kStream;
+        const int steps = (min(y_len - row, kStream) + 15) / 16;
+        ok = warp_wait(&B.full[slot], (j / kBwdStages) & 1, abort) && warp_wait(&B.d_full[b], (j >> 1) & 1, abort);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t z0 = desc_mn<kStreamChunk>(smem_addr(ring + slot * 2 * kOne)), z1 = z0 + (kOne >> 4);
+        const uint32_t d = tm + b * T::kBuf;
+        if (one) {
+            if (KEYS) add(tm + T::kAcc0, d, z1, steps, j > 0);
+            add(tm + T::kAcc1, d + T::kDs, z0, steps, j > 0);
+            mma_commit(KEYS ? &B.s_free[b] : &B.acc_done[b]);
+            mma_commit(&B.empty[slot]);
+            if (j + 1 == st.n) mma_commit(&B.acc_full);
+        }
+        __syncwarp();
+    }
+    if (!ok) drain_mmas(one, &B.drain[1]);
+}
+
 // mx0, mx1: maps of the kept tensors, my0, my1 of the streamed ones (boxes of 64 rows).
 template <int DP, bool KEYS>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(kAttnThreads, 1)
 pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constant__ CUtensorMap mx1,
                    const __grid_constant__ CUtensorMap my0, const __grid_constant__ CUtensorMap my1,
                    const __grid_constant__ AttnParams P) {
-    constexpr int kC = kChunks<DP>;
-    constexpr uint32_t kKept = kC * kChunkBytes, kOne = kC * kStreamChunk;     // bytes of one kept / streamed tile
     extern __shared__ uint8_t raw[];
     __shared__ BwdBars B;
-    uint8_t *kept = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023), *ring = kept + 2 * kKept;
-    volatile int *abort = &B.abort;
+    uint8_t *kept = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023), *ring = kept + 2 * kChunks<DP> * kChunkBytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.y, share = P.Hq / P.Hkv;
+    const int h = blockIdx.y;
     if (warp == 9) {
         const Work w = find_work(P, KEYS, blockIdx.x, kTile);
         if (lane == 0) {
@@ -850,8 +1017,13 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
             mbar_init(smem_addr(&B.tail), 1);
             mbar_init(smem_addr(&B.xfull), 1);
             mbar_init(smem_addr(&B.acc_full), 1);
-            mbar_init(smem_addr(&B.drain), 1);
-            for (int t = 0; t < 2; ++t) mbar_init(smem_addr(&B.s_full[t]), 1), mbar_init(smem_addr(&B.d_full[t]), 4);
+            for (int t = 0; t < 2; ++t) {
+                mbar_init(smem_addr(&B.s_full[t]), 1);
+                mbar_init(smem_addr(&B.s_free[t]), KEYS ? 1 : 4);
+                mbar_init(smem_addr(&B.d_full[t]), 4);
+                mbar_init(smem_addr(&B.acc_done[t]), 1);
+                mbar_init(smem_addr(&B.drain[t]), 1);
+            }
             fence_mbar_init();
             prefetch_tmap(&mx0);
             prefetch_tmap(&mx1);
@@ -870,134 +1042,15 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
     __syncthreads();
     tc_fence_after();
     const Stream st = stream_of<KEYS>(P, w);
-    const int y_len = KEYS ? w.lq : w.lk;                   // streamed rows of the sequence
     if (warp < 8) {
+        regs_up<224>();
         bwd_group<DP, KEYS>(P, B, w, st, warp >> 2, h);
-    } else if (warp == 8 && st.n > 0) {
-        // ---- loads
-        const int x_row = (KEYS ? w.k0 : w.q0) + w.row, x_head = h;
-        if (lane == 0) {
-            mbar_arrive_expect_tx(smem_addr(&B.xfull), 2 * kKept);
-            for (int t = 0; t < 2; ++t)
-                for (int c = 0; c < kC; ++c)
-                    for (int half = 0; half < 2; ++half)
-                        tma_load_3d(smem_addr(kept + t * kKept + c * kChunkBytes + half * kStreamChunk), t ? &mx1 : &mx0,
-                                    smem_addr(&B.xfull), 64 * c, x_head, x_row + half * kStream);
-        }
-        int f = 0, tails = 0;
-        bool ok = true;
-        for (; f < st.n; ++f) {
-            const int slot = f % kBwdStages;
-            ok = warp_wait(&B.empty[slot], ((f / kBwdStages) & 1) ^ 1, abort);
-            if (!ok) break;
-            const int row = (st.first + (KEYS ? f % st.per_head : f)) * kStream;
-            const int y_head = KEYS ? h * share + f / st.per_head : h / share;
-            const int y_row = (KEYS ? w.q0 : w.k0) + row;
-            const int valid = min(y_len - row, kStream);
-            uint8_t *dst = ring + slot * 2 * kOne;
-            const bool clean = valid < kStream;             // the sequence's last tile: zeros behind it
-            uint64_t *bar = clean ? &B.tail : &B.full[slot];
-            if (KEYS) {
-                const float *src = P.lse2 + (int64_t)y_head * P.Nq + y_row;
-                const float *srd = P.delta + (int64_t)y_head * P.Nq + y_row;
-#pragma unroll
-                for (int e = lane; e < kStream; e += 32) {
-                    const bool in = e < valid;
-                    cp_async4(smem_addr(&B.stat[slot][0][e]), in ? src + e : src, in);
-                    cp_async4(smem_addr(&B.stat[slot][1][e]), in ? srd + e : srd, in);
-                }
-                cp_async_arrive(smem_addr(&B.full[slot]));
-            }
-            if (lane == 0) {
-                mbar_arrive_expect_tx(smem_addr(bar), 2 * kOne);
-                for (int t = 0; t < 2; ++t)
-                    for (int c = 0; c < kC; ++c)
-                        tma_load_3d(smem_addr(dst + t * kOne + c * kStreamChunk), t ? &my1 : &my0, smem_addr(bar), 64 * c,
-                                    y_head, y_row);
-            }
-            __syncwarp();
-            if (clean) {
-                ok = warp_wait(&B.tail, tails & 1, abort);
-                if (!ok) {
-                    int never = 0;
-                    block_wait(&B.tail, tails & 1, &never);
-                    break;
-                }
-                ++tails;
-                for (int t = 0; t < 2; ++t) zero_rows<kC, kStreamChunk>(dst + t * kOne, valid, (valid + 15) & ~15);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&B.full[slot]));
-            }
-        }
-        if (!ok) {   // a wait gave up: the copies in flight still land before the block ends
-            int never = 0;
-            block_wait(&B.xfull, 0, &never);
-            for (int s = max(f - kBwdStages, 0); s < f; ++s)
-                block_wait(&B.full[s % kBwdStages], (s / kBwdStages) & 1, &never);
-        }
-    } else if (warp == 9 && st.n > 0) {
-        // ---- MMAs
-        constexpr uint32_t kIdS = idesc_bf16_f32(kTile, kStream), kIdA = idesc_b_mn(kTile, DP);
-        const uint32_t one = elect_one(), tm = B.tmem;
-        const uint32_t d_x0 = desc_k(smem_addr(kept)), d_x1 = desc_k(smem_addr(kept + kKept));
-        const uint32_t d_y0 = desc_k(smem_addr(ring)), d_y1 = desc_k(smem_addr(ring + kOne));
-        const uint32_t d_z0 = desc_mn<kStreamChunk>(smem_addr(ring)), d_z1 = desc_mn<kStreamChunk>(smem_addr(ring + kOne));
-        auto slot_of = [](int f) { return (uint32_t)(f % kBwdStages) * (2 * kOne >> 4); };
-        auto wait_full = [&](int f) { return warp_wait(&B.full[f % kBwdStages], (f / kBwdStages) & 1, abort); };
-        auto issue_s = [&](int j) {
-            const uint32_t d = tm + (j & 1) * 128, y0 = d_y0 + slot_of(j), y1 = d_y1 + slot_of(j);
-            if (one) {
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-                    mma_ss(d, d_x0 + step_k<kChunkBytes>(k), y0 + step_k<kStreamChunk>(k), kDescHi, kDescHi, kIdS, k > 0);
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-                    mma_ss(d + 64, d_x1 + step_k<kChunkBytes>(k), y1 + step_k<kStreamChunk>(k), kDescHi, kDescHi, kIdS, k > 0);
-                mma_commit(&B.s_full[j & 1]);
-            }
-            __syncwarp();
-        };
-        // kept rows += A (tensor memory) times the streamed tile at z
-        auto issue_acc = [&](uint32_t acc, uint32_t a, uint32_t z, int steps, bool add) {
-            mma_ts(acc, a, z, kDescHi, kIdA, add);
-            if (steps == kStream / 16) {
-#pragma unroll
-                for (int k = 1; k < kStream / 16; ++k) mma_ts(acc, a + 8 * k, z + step_mn(k), kDescHi, kIdA, true);
-            } else {
-                for (int k = 1; k < steps; ++k) mma_ts(acc, a + 8 * k, z + step_mn(k), kDescHi, kIdA, true);
-            }
-        };
-        bool ok = warp_wait(&B.xfull, 0, abort);
-        for (int j = 0; j < 2 && j < st.n && ok; ++j) {
-            ok = wait_full(j);
-            tc_fence_after();
-            if (ok) issue_s(j);
-        }
-        for (int j = 0; j < st.n && ok; ++j) {
-            const int b = j & 1, row = (st.first + (KEYS ? j % st.per_head : j)) * kStream;
-            const int steps = (min(y_len - row, kStream) + 15) / 16;
-            const uint32_t d = tm + b * 128;
-            ok = warp_wait(&B.d_full[b], (j >> 1) & 1, abort);
-            if (!ok) break;
-            tc_fence_after();
-            if (one) {
-                if (KEYS) issue_acc(tm + 256, d, d_z1 + slot_of(j), steps, j > 0);
-                issue_acc(tm + 384, d + 64, d_z0 + slot_of(j), steps, j > 0);
-                mma_commit(&B.empty[j % kBwdStages]);
-                if (j + 1 == st.n) mma_commit(&B.acc_full);
-            }
-            __syncwarp();
-            if (j + 2 < st.n) {
-                ok = wait_full(j + 2);
-                tc_fence_after();
-                if (ok) issue_s(j + 2);
-            }
-        }
-        if (!ok) {   // MMAs in flight finish before their tensor memory is freed
-            int never = 0;
-            if (one) mma_commit(&B.drain);
-            warp_wait(&B.drain, 0, &never);
+    } else {
+        regs_down<56>();
+        if (st.n > 0) {
+            if (warp == 8) bwd_load<DP, KEYS>(P, B, w, st, mx0, mx1, my0, my1, kept, ring, h);
+            else if (warp == 9) bwd_scores<DP, KEYS>(B, st, kept, ring);
+            else if (warp == 10) bwd_sums<DP, KEYS>(B, st, ring, KEYS ? w.lq : w.lk);
         }
     }
     __syncwarp();

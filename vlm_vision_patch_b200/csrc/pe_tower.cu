@@ -174,7 +174,7 @@ template <class Kernel>
 bool ready_to_launch(Kernel kern, size_t smem) {
     cudaFuncAttributes at;
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess &&
-           cudaFuncGetAttributes(&at, kern) == cudaSuccess && at.numRegs * kFwdThreads >= 256 * 224 + 128 * 56;
+           cudaFuncGetAttributes(&at, kern) == cudaSuccess && at.numRegs * kAttnThreads >= 256 * 224 + 128 * 56;
 }
 
 // Tiles of `rows` rows that n rows in n_seq sequences can make, at most.
@@ -457,7 +457,7 @@ pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, 
         auto kern = pe_attn_fwd_kernel<decltype(dp)::value>;
         if (!ready_to_launch(kern, S::kSmem)) return PE_ERR_CUDA;
         const dim3 grid(max_tiles(Nq, n_seq, 2 * kTile), (unsigned)a->Hq);
-        kern<<<grid, kFwdThreads, S::kSmem, (cudaStream_t)stream>>>(mq, mk, mv, P);
+        kern<<<grid, kAttnThreads, S::kSmem, (cudaStream_t)stream>>>(mq, mk, mv, P);
         return finish(cudaGetLastError());
     });
 }
@@ -495,8 +495,8 @@ pe_status pe_attention_backward(pe_attention *a, int n_seq, const int32_t *cu_q,
     P.dk = heads_ptr(dk, Nk, a->Hkv);
     P.dv = heads_ptr(dv, Nk, a->Hkv);
     P.lse = const_cast<float *>(lse);
-    P.lse2 = static_cast<float *>(ws);
-    P.delta = P.lse2 + (int64_t)a->Hq * Nq;
+    P.nlse2 = static_cast<float *>(ws);
+    P.ndelta = P.nlse2 + (int64_t)a->Hq * Nq;
     cudaStream_t st = (cudaStream_t)stream;
     CUtensorMap mq, mk, mv, md;
     if (Nq > 0 && (!make_heads_tmap(&mq, q, Nq, a->Hq, D, kStream) || !make_heads_tmap(&md, dout, Nq, a->Hq, D, kStream)))
@@ -511,16 +511,15 @@ pe_status pe_attention_backward(pe_attention *a, int n_seq, const int32_t *cu_q,
         auto dq_kern = pe_attn_bwd_kernel<DP, false>;
         auto dkv_kern = pe_attn_bwd_kernel<DP, true>;
         for (auto kern : {dq_kern, dkv_kern})
-            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBwdSmem<DP>) != cudaSuccess)
-                return PE_ERR_CUDA;
+            if (!ready_to_launch(kern, kBwdSmem<DP>)) return PE_ERR_CUDA;
         if (Nq > 0) {
             const dim3 grid(max_tiles(Nq, n_seq, kTile), (unsigned)a->Hq);
-            dq_kern<<<grid, kBwdThreads, kBwdSmem<DP>, st>>>(mq, md, mk, mv, P);
+            dq_kern<<<grid, kAttnThreads, kBwdSmem<DP>, st>>>(mq, md, mk, mv, P);
             if (cudaGetLastError() != cudaSuccess) return PE_ERR_CUDA;
         }
         if (Nk > 0) {
             const dim3 grid(max_tiles(Nk, n_seq, kTile), (unsigned)a->Hkv);
-            dkv_kern<<<grid, kBwdThreads, kBwdSmem<DP>, st>>>(mk, mv, mq, md, P);
+            dkv_kern<<<grid, kAttnThreads, kBwdSmem<DP>, st>>>(mk, mv, mq, md, P);
         }
         return finish(cudaGetLastError());
     });
