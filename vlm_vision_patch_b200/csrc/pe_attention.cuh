@@ -16,26 +16,39 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// mbar_wait for barriers that only this block arrives on (block-scope acquire),
-// on the critical path of a softmax: the clock is read only once the wait has
-// failed a few times.
-__device__ __forceinline__ bool block_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_addr(bar)), "r"(parity)
-            : "memory");
-        if (ok) return true;
-    }
-    return mbar_wait(smem_addr(bar), parity, abort);
+// Clock ticks after which a wait gives up: 2 s at the highest clock.
+constexpr long long kWaitClocks = 4000000000ll;
+
+__device__ __forceinline__ bool try_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
-// A whole warp waits; all lanes go on, or none (a wait gave up).
+
+// A converged warp waits for a phase of a barrier that only this block arrives on;
+// bounded like mbar_wait.  Every branch is the whole warp's, so a wait that is
+// already over costs one look and one vote (a loop that lanes could leave one by
+// one cost the issuing warps about 200 clocks per wait more).
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    return __all_sync(0xffffffffu, block_wait(bar, parity, abort));
+    if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
+    const long long t0 = clock64();
+    while (!__all_sync(0xffffffffu, try_wait(bar, parity))) {
+        if (__any_sync(0xffffffffu, *abort != 0 || clock64() - t0 > kWaitClocks)) {
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+// After an abort: waits for what is in flight, by the clock alone.
+__device__ __forceinline__ void warp_drain(uint64_t *bar, uint32_t parity) {
+    int never = 0;
+    warp_wait(bar, parity, &never);
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int32_t x, int32_t y,
@@ -327,10 +340,9 @@ struct FwdBars {
 
 // MMAs in flight finish before their tensor memory is freed.
 __device__ __forceinline__ void drain_mmas(uint32_t one, uint64_t *bar) {
-    int never = 0;
     if (one) mma_commit(bar);
     __syncwarp();
-    warp_wait(bar, 0, &never);
+    warp_drain(bar, 0);
 }
 
 // p = 2^(s sl2 - base) of one row of 16 C scores, as bf16 pairs; returns the row's
@@ -499,8 +511,7 @@ __device__ __forceinline__ void fwd_load(const AttnParams &P, FwdBars &B, const 
         if (clean) {
             ok = warp_wait(&B.tail, 0, abort);
             if (!ok) {
-                int never = 0;
-                block_wait(&B.tail, 0, &never);
+                warp_drain(&B.tail, 0);
                 break;
             }
             zero_rows<S::kC, S::kChunk>(dst, valid, (valid + 15) & ~15);
@@ -510,10 +521,8 @@ __device__ __forceinline__ void fwd_load(const AttnParams &P, FwdBars &B, const 
         }
     }
     if (!ok) {   // a wait gave up: the copies in flight still land before the block ends
-        int never = 0;
-        block_wait(&B.qfull, 0, &never);
-        for (int s = max(f - S::kStages, 0); s < f; ++s)
-            block_wait(&B.full[s % S::kStages], (s / S::kStages) & 1, &never);
+        warp_drain(&B.qfull, 0);
+        for (int s = max(f - S::kStages, 0); s < f; ++s) warp_drain(&B.full[s % S::kStages], (s / S::kStages) & 1);
     }
 }
 
@@ -907,8 +916,7 @@ __device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const 
         if (clean) {
             ok = warp_wait(&B.tail, tails & 1, abort);
             if (!ok) {
-                int never = 0;
-                block_wait(&B.tail, tails & 1, &never);
+                warp_drain(&B.tail, tails & 1);
                 break;
             }
             ++tails;
@@ -919,10 +927,8 @@ __device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const 
         }
     }
     if (!ok) {   // a wait gave up: the copies in flight still land before the block ends
-        int never = 0;
-        block_wait(&B.xfull, 0, &never);
-        for (int s = max(f - kBwdStages, 0); s < f; ++s)
-            block_wait(&B.full[s % kBwdStages], (s / kBwdStages) & 1, &never);
+        warp_drain(&B.xfull, 0);
+        for (int s = max(f - kBwdStages, 0); s < f; ++s) warp_drain(&B.full[s % kBwdStages], (s / kBwdStages) & 1);
     }
 }
 
