@@ -208,7 +208,7 @@ struct AttnParams {
     float scale;
     HeadsPtr q, k, v, out, dout, dq, dk, dv;
     float *lse;                   // [Hq, Nq]
-    float *nlse2, *ndelta;        // [Hq, Nq]: -lse * log2(e), and -dout . out (backward)
+    uint4 *stat;                  // [Hq, Nq]: -lse / scale and -dout . out, three bf16 and a 0 each (backward)
     int *err;
 };
 
@@ -294,6 +294,12 @@ __host__ __device__ constexpr uint32_t step_k(int k) { return (uint32_t)((k >> 2
 template <int CHUNK>
 __device__ __forceinline__ uint32_t desc_mn(uint32_t tile) { return (uint32_t)smem_desc(tile, CHUNK, 1024, kLayoutSw128); }
 __host__ __device__ constexpr uint32_t step_mn(int k) { return (uint32_t)(k * 2048) >> 4; }
+// An operand of 16 columns without swizzle, 8 columns (16 bytes a row, rows one
+// behind the other) at `tile` and 8 at tile + next.
+__device__ __forceinline__ uint32_t desc_flat(uint32_t tile, uint32_t next) {
+    return (uint32_t)smem_desc(tile, next, 128, kLayoutInterleave);
+}
+constexpr uint32_t kDescHiFlat = (128u >> 4) | (1u << 14);
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | ((uint32_t)kLayoutSw128 << 29);
 __host__ __device__ constexpr uint32_t idesc_b_mn(int M, int N) { return idesc_bf16_f32(M, N) | (1u << 16); }
 
@@ -683,32 +689,44 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
 // The streamed tiles hold 64 rows, so that two pairs (s, dp) fit in tensor
 // memory beside the sums: warps 0-3 work on one while the tensor cores fill the
 // other for warps 4-7.  p and ds go back to tensor memory as bf16 and are the A
-// operands of the sums.  Scores and sums are issued by a warp each, as the
-// forward pass's tiles are.  For queries ds has columns of its own, so that the
-// next scores need not wait for the sums; for keys the two sums leave no room.
+// operands of the sums.
+//
+// For keys, lse and delta belong to columns: each thread would need all 64 pairs
+// of every tile from shared memory (that took as long as the products).  Instead
+// each goes into the product itself, as one more k-step: every kept row times
+// (1, 1, 1, 0 ...), every query times its statistic as a sum of three bf16, which
+// is 24 bits.  So s arrives as s - lse / scale and dp as dp - delta.
 
 constexpr int kStream = 64;                       // streamed rows per tile
 constexpr int kStreamChunk = kStream * 128;       // bytes of 64 rows of 64 bf16
 constexpr int kBwdStages = 4;
 
 template <int DP>
-constexpr size_t kBwdSmem = (size_t)kChunks<DP> * (2 * kChunkBytes + kBwdStages * 2 * kStreamChunk) + 1024;
+constexpr uint32_t kBwdTiles = kChunks<DP> * (2 * kChunkBytes + kBwdStages * 2 * kStreamChunk);
+// Behind the tiles: the two selectors of the statistics (128 rows of 16 bf16), the
+// statistics of each stage's 64 queries (8 bf16), and 64 rows of zeros.
+constexpr uint32_t kSelect = kTile * 32, kStats = kStream * 16, kExtra = 2 * kSelect + (kBwdStages + 1) * kStats;
+template <int DP>
+constexpr size_t kBwdSmem = (size_t)kBwdTiles<DP> + kExtra + 1024;
 
 struct BwdBars {
-    uint64_t full[kBwdStages], empty[kBwdStages], tail, xfull, s_full[2], s_free[2], d_full[2], acc_done[2], acc_full, drain[2];
+    uint64_t full[kBwdStages], empty[kBwdStages], tail, xfull, s_full[2], s_free[2], d_full[2], acc_done[2], acc_full, drain[3];
     uint32_t tmem;
     int abort;
     Work w;
-    alignas(16) float stat[kBwdStages][2][kStream];   // nlse2 and ndelta of the streamed queries
 };
 
-// 4 bytes to shared memory without waiting; zero when !take.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const float *src, bool take) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(take ? 4 : 0) : "memory");
+// `bytes` contiguous bytes to shared memory (both 16-byte aligned, a multiple of 16).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
-// This thread's copies so far, once they have landed, count as one arrival.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+
+// v as a sum of three bf16 (24 bits), the second word's high half 0.
+__device__ __forceinline__ uint2 split3(float v) {
+    const float h = __bfloat162float(__float2bfloat16_rn(v)), m = __bfloat162float(__float2bfloat16_rn(v - h));
+    return make_uint2(pack_bf16x2(h, m), pack_bf16x2(v - h - m, 0.f));
 }
 
 // The streamed tiles of one block: for keys, the query tiles of every head that
@@ -732,24 +750,35 @@ __device__ __forceinline__ Stream stream_of(const AttnParams &P, const Work &w) 
     return st;
 }
 
-template <bool KEYS>
-struct BwdCols {                                  // of buffer b: s at b * kBuf, dp 64 behind it, ds (and p in place of s)
-    static constexpr uint32_t kBuf = KEYS ? 128 : 160, kDs = KEYS ? 64 : 128, kAcc0 = 256, kAcc1 = 384;
+// Columns of tensor memory.  Buffer b: s at b * 128, dp 64 behind it.  For queries
+// each buffer's ds has columns of its own.  For keys p and ds of both buffers
+// share one place, so a group stores them once the sums have read the last; with
+// head sizes above 96 the two sums leave no room for that, and p and ds take the
+// place of s and dp (the next scores of that buffer then wait for the sums).
+template <int DP, bool KEYS>
+struct BwdCols {
+    static constexpr bool kAlias = KEYS && DP > 96, kShared = KEYS && !kAlias;
+    static constexpr uint32_t kBuf = 128;
+    static constexpr uint32_t kP = 256, kDs = KEYS ? 288 : 256;         // of the shared place, or of ds of buffer 0
+    static constexpr uint32_t kAcc0 = kAlias ? 256 : 320, kAcc1 = KEYS ? kAcc0 + DP : 320;
+    static_assert(kAcc1 + DP <= 512, "tensor memory");
+    __device__ static uint32_t p(int b) { return kAlias ? b * kBuf : kP; }
+    __device__ static uint32_t ds(int b) { return kAlias ? b * kBuf + 64 : (kShared ? kDs : kDs + 32 * b); }
 };
 
 // p and ds of every second streamed tile, then half of the results; the 128
 // threads of group g, one kept row each.
 template <int DP, bool KEYS>
 __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const Work &w, const Stream &st, int g, int h) {
-    using T = BwdCols<KEYS>;
+    using T = BwdCols<DP, KEYS>;
     volatile int *abort = &B.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t lanes = B.tmem + ((uint32_t)(warp & 3) << 21);
-    const uint32_t ts = lanes + g * T::kBuf, td = ts + T::kDs;
+    const uint32_t ts = lanes + g * T::kBuf, tp = lanes + T::p(g), td = lanes + T::ds(g);
     const int i = w.row + (warp & 3) * 32 + lane;           // kept row within the sequence
     const bool mine = i < (KEYS ? w.lk : w.lq);
     const float2 sl2 = both(P.scale * kLog2e);
-    float nlse2 = 0.f, ndelta = 0.f;
+    float nlse2 = 0.f, ndelta = 0.f;                        // of a kept query: -lse log2(e), -delta
     int limit = 0;
     if (!KEYS) {
         limit = mine ? keys_seen(P, w, i) : 0;
@@ -763,18 +792,17 @@ __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const
                 for (int k = 0; k < 4; ++k)
                     ndelta -= bf16lo_to_f32(x[k]) * bf16lo_to_f32(y[k]) + bf16hi_to_f32(x[k]) * bf16hi_to_f32(y[k]);
             }
-            // a row that sees no key has lse = -inf; +inf gives it p = 0 for every key
-            nlse2 = limit > 0 ? -P.lse[at] * kLog2e : -INFINITY;
+            nlse2 = -P.lse[at] * kLog2e;
             if (g == 0) {
-                P.nlse2[at] = nlse2;
-                P.ndelta[at] = ndelta;
+                // a row that sees no key has lse = -inf; with a large finite value its p is 0 and no product inf * 0
+                const uint2 u = split3(limit > 0 ? -P.lse[at] / P.scale : -1e30f), v = split3(ndelta);
+                P.stat[at] = make_uint4(u.x, u.y, v.x, v.y);
             }
         }
     }
     const int shift = w.lk - w.lq;
     for (int j = g; j < st.n; j += 2) {
-        const int n = j >> 1, stage = j % kBwdStages;
-        if (KEYS && !warp_wait(&B.full[stage], (j / kBwdStages) & 1, abort)) return;
+        const int n = j >> 1;
         if (!warp_wait(&B.s_full[g], n & 1, abort)) return;
         tc_fence_after();
         const int y = (st.first + (KEYS ? j % st.per_head : j)) * kStream;      // first streamed row
@@ -786,7 +814,7 @@ __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const
         }
         tmem_ld_wait_for(s);
         tmem_ld_wait_for(d);
-        if (!KEYS) {
+        if (!T::kAlias) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&B.s_free[g]));
@@ -797,36 +825,28 @@ __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                float4 L = make_float4(nlse2, nlse2, nlse2, nlse2), D = make_float4(ndelta, ndelta, ndelta, ndelta);
-                if (KEYS) {
-                    L = *reinterpret_cast<const float4 *>(&B.stat[stage][0][16 * c + e]);
-                    D = *reinterpret_cast<const float4 *>(&B.stat[stage][1][16 * c + e]);
+            for (int e = 0; e < 16; e += 2) {
+                const float2 sc = make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+                const float2 dp = make_float2(__uint_as_float(d[c][e]), __uint_as_float(d[c][e + 1]));
+                const float2 x = KEYS ? mul2(sc, sl2) : fma2(sc, sl2, both(nlse2));
+                float2 p = make_float2(ex2(x.x), ex2(x.y));
+                float2 q = mul2(p, KEYS ? dp : add2(dp, both(ndelta)));
+                if (cut) {
+                    const int col = y + 16 * c + e;
+                    if (KEYS ? col < i - shift : col >= limit) p.x = q.x = 0.f;
+                    if (KEYS ? col + 1 < i - shift : col + 1 >= limit) p.y = q.y = 0.f;
                 }
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int at = e + 2 * k;
-                    const float2 x = fma2(make_float2(__uint_as_float(s[c][at]), __uint_as_float(s[c][at + 1])), sl2,
-                                          k ? make_float2(L.z, L.w) : make_float2(L.x, L.y));
-                    float2 p = make_float2(ex2(x.x), ex2(x.y));
-                    float2 q = mul2(p, add2(make_float2(__uint_as_float(d[c][at]), __uint_as_float(d[c][at + 1])),
-                                            k ? make_float2(D.z, D.w) : make_float2(D.x, D.y)));
-                    if (cut) {
-                        const int col = y + 16 * c + at;
-                        if (KEYS ? col < i - shift : col >= limit) p.x = q.x = 0.f;
-                        if (KEYS ? col + 1 < i - shift : col + 1 >= limit) p.y = q.y = 0.f;
-                    }
-                    if (KEYS) pp[c][at / 2] = pack_bf16x2(p.x, p.y);
-                    pd[c][at / 2] = pack_bf16x2(q.x, q.y);
-                }
+                if (KEYS) pp[c][e / 2] = pack_bf16x2(p.x, p.y);
+                pd[c][e / 2] = pack_bf16x2(q.x, q.y);
             }
-        if (!KEYS && n > 0) {                               // the sums have read the last ds
-            if (!warp_wait(&B.acc_done[g], (n - 1) & 1, abort)) return;
+        // the sums have read what was in its place
+        if (T::kShared ? j > 0 : !T::kAlias && n > 0) {
+            if (!warp_wait(&B.acc_done[T::kShared ? 0 : g], ((T::kShared ? j : n) - 1) & 1, abort)) return;
             tc_fence_after();
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            if (KEYS) tmem_st_x8(ts + 8 * c, pp[c]);
+            if (KEYS) tmem_st_x8(tp + 8 * c, pp[c]);
             tmem_st_x8(td + 8 * c, pd[c]);
         }
         tmem_st_wait();
@@ -866,7 +886,7 @@ __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const
 template <int DP, bool KEYS>
 __device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const Work &w, const Stream &st,
                                          const CUtensorMap &mx0, const CUtensorMap &mx1, const CUtensorMap &my0,
-                                         const CUtensorMap &my1, uint8_t *kept, uint8_t *ring, int h) {
+                                         const CUtensorMap &my1, uint8_t *kept, uint8_t *ring, uint8_t *stats, int h) {
     constexpr int kC = kChunks<DP>;
     constexpr uint32_t kKept = kC * kChunkBytes, kOne = kC * kStreamChunk;     // bytes of one kept / streamed tile
     volatile int *abort = &B.abort;
@@ -894,19 +914,11 @@ __device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const 
         uint8_t *dst = ring + slot * 2 * kOne;
         const bool clean = valid < kStream;                 // the sequence's last tile: zeros behind it
         uint64_t *bar = clean ? &B.tail : &B.full[slot];
-        if (KEYS) {
-            const float *src = P.nlse2 + (int64_t)y_head * P.Nq + y_row;
-            const float *srd = P.ndelta + (int64_t)y_head * P.Nq + y_row;
-#pragma unroll
-            for (int e = lane; e < kStream; e += 32) {
-                const bool in = e < valid;
-                cp_async4(smem_addr(&B.stat[slot][0][e]), in ? src + e : src, in);
-                cp_async4(smem_addr(&B.stat[slot][1][e]), in ? srd + e : srd, in);
-            }
-            cp_async_arrive(smem_addr(&B.full[slot]));
-        }
         if (lane == 0) {
-            mbar_arrive_expect_tx(smem_addr(bar), 2 * kOne);
+            mbar_arrive_expect_tx(smem_addr(bar), 2 * kOne + (KEYS ? valid * 16 : 0));
+            if (KEYS)
+                bulk_load(smem_addr(stats + slot * kStats), P.stat + (int64_t)y_head * P.Nq + y_row, valid * 16,
+                          smem_addr(bar));
             for (int t = 0; t < 2; ++t)
                 for (int c = 0; c < kC; ++c)
                     tma_load_3d(smem_addr(dst + t * kOne + c * kStreamChunk), t ? &my1 : &my0, smem_addr(bar), 64 * c,
@@ -920,7 +932,10 @@ __device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const 
                 break;
             }
             ++tails;
-            for (int t = 0; t < 2; ++t) zero_rows<kC, kStreamChunk>(dst + t * kOne, valid, (valid + 15) & ~15);
+            const int end = (valid + 15) & ~15;
+            for (int t = 0; t < 2; ++t) zero_rows<kC, kStreamChunk>(dst + t * kOne, valid, end);
+            if (KEYS && lane < end - valid)
+                *reinterpret_cast<uint4 *>(stats + slot * kStats + (valid + lane) * 16) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&B.full[slot]));
@@ -932,18 +947,20 @@ __device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const 
     }
 }
 
-// s and dp of every streamed tile (one warp).
+// s and dp of every second streamed tile, buffer b (one warp each: while one waits
+// for room, the other keeps the tensor cores busy).
 template <int DP, bool KEYS>
-__device__ __forceinline__ void bwd_scores(BwdBars &B, const Stream &st, uint8_t *kept, uint8_t *ring) {
-    using T = BwdCols<KEYS>;
+__device__ __forceinline__ void bwd_scores(BwdBars &B, const Stream &st, uint8_t *kept, uint8_t *ring, uint8_t *select,
+                                           uint8_t *stats, int b) {
+    using T = BwdCols<DP, KEYS>;
     constexpr int kC = kChunks<DP>;
     constexpr uint32_t kKept = kC * kChunkBytes, kOne = kC * kStreamChunk, kIdS = idesc_bf16_f32(kTile, kStream);
     volatile int *abort = &B.abort;
     const uint32_t one = elect_one(), tm = B.tmem;
     const uint32_t x0 = desc_k(smem_addr(kept)), x1 = desc_k(smem_addr(kept + kKept));
     bool ok = warp_wait(&B.xfull, 0, abort);
-    for (int j = 0; j < st.n && ok; ++j) {
-        const int b = j & 1, n = j >> 1, slot = j % kBwdStages;
+    for (int j = b; j < st.n && ok; j += 2) {
+        const int n = j >> 1, slot = j % kBwdStages;
         ok = warp_wait(&B.full[slot], (j / kBwdStages) & 1, abort) && (n == 0 || warp_wait(&B.s_free[b], (n - 1) & 1, abort));
         if (!ok) break;
         tc_fence_after();
@@ -955,17 +972,23 @@ __device__ __forceinline__ void bwd_scores(BwdBars &B, const Stream &st, uint8_t
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k)
                 mma_ss(d + 64, x1 + step_k<kChunkBytes>(k), y1 + step_k<kStreamChunk>(k), kDescHi, kDescHi, kIdS, k > 0);
+            if (KEYS) {
+                const uint32_t at = smem_addr(stats + slot * kStats), zeros = smem_addr(stats + kBwdStages * kStats);
+                const uint32_t z = desc_flat(at, zeros - at), sel = desc_flat(smem_addr(select), kTile * 16);
+                mma_ss(d, sel, z, kDescHiFlat, kDescHiFlat, kIdS, true);
+                mma_ss(d + 64, sel + (kSelect >> 4), z, kDescHiFlat, kDescHiFlat, kIdS, true);
+            }
             mma_commit(&B.s_full[b]);
         }
         __syncwarp();
     }
-    if (!ok) drain_mmas(one, &B.drain[0]);
+    if (!ok) drain_mmas(one, &B.drain[b]);
 }
 
 // The sums over the streamed tiles (one warp).
 template <int DP, bool KEYS>
 __device__ __forceinline__ void bwd_sums(BwdBars &B, const Stream &st, uint8_t *ring, int y_len) {
-    using T = BwdCols<KEYS>;
+    using T = BwdCols<DP, KEYS>;
     constexpr uint32_t kOne = kChunks<DP> * kStreamChunk, kIdA = idesc_b_mn(kTile, DP);
     volatile int *abort = &B.abort;
     const uint32_t one = elect_one(), tm = B.tmem;
@@ -987,17 +1010,16 @@ __device__ __forceinline__ void bwd_sums(BwdBars &B, const Stream &st, uint8_t *
         if (!ok) break;
         tc_fence_after();
         const uint32_t z0 = desc_mn<kStreamChunk>(smem_addr(ring + slot * 2 * kOne)), z1 = z0 + (kOne >> 4);
-        const uint32_t d = tm + b * T::kBuf;
         if (one) {
-            if (KEYS) add(tm + T::kAcc0, d, z1, steps, j > 0);
-            add(tm + T::kAcc1, d + T::kDs, z0, steps, j > 0);
-            mma_commit(KEYS ? &B.s_free[b] : &B.acc_done[b]);
+            if (KEYS) add(tm + T::kAcc0, tm + T::p(b), z1, steps, j > 0);
+            add(tm + T::kAcc1, tm + T::ds(b), z0, steps, j > 0);
+            mma_commit(T::kAlias ? &B.s_free[b] : &B.acc_done[T::kShared ? 0 : b]);
             mma_commit(&B.empty[slot]);
             if (j + 1 == st.n) mma_commit(&B.acc_full);
         }
         __syncwarp();
     }
-    if (!ok) drain_mmas(one, &B.drain[1]);
+    if (!ok) drain_mmas(one, &B.drain[2]);
 }
 
 // mx0, mx1: maps of the kept tensors, my0, my1 of the streamed ones (boxes of 64 rows).
@@ -1009,6 +1031,7 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
     extern __shared__ uint8_t raw[];
     __shared__ BwdBars B;
     uint8_t *kept = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023), *ring = kept + 2 * kChunks<DP> * kChunkBytes;
+    uint8_t *select = kept + kBwdTiles<DP>, *stats = select + 2 * kSelect;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.y;
     if (warp == 9) {
@@ -1017,7 +1040,7 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
             B.w = w;
             B.abort = 0;
             for (int i = 0; i < kBwdStages; ++i) {
-                mbar_init(smem_addr(&B.full[i]), KEYS ? 33 : 1);
+                mbar_init(smem_addr(&B.full[i]), 1);
                 mbar_init(smem_addr(&B.empty[i]), 1);
             }
             mbar_init(smem_addr(&B.tail), 1);
@@ -1025,11 +1048,11 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
             mbar_init(smem_addr(&B.acc_full), 1);
             for (int t = 0; t < 2; ++t) {
                 mbar_init(smem_addr(&B.s_full[t]), 1);
-                mbar_init(smem_addr(&B.s_free[t]), KEYS ? 1 : 4);
+                mbar_init(smem_addr(&B.s_free[t]), BwdCols<DP, KEYS>::kAlias ? 1 : 4);
                 mbar_init(smem_addr(&B.d_full[t]), 4);
                 mbar_init(smem_addr(&B.acc_done[t]), 1);
-                mbar_init(smem_addr(&B.drain[t]), 1);
             }
+            for (int t = 0; t < 3; ++t) mbar_init(smem_addr(&B.drain[t]), 1);
             fence_mbar_init();
             prefetch_tmap(&mx0);
             prefetch_tmap(&mx1);
@@ -1040,6 +1063,17 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
     __syncthreads();
     const Work w = B.w;
     if (w.row < 0) return;
+    if (KEYS) {
+        // 1 in columns 0, 1, 2 selects the first statistic, in 4, 5, 6 the second; the rest is 0
+        for (int i = threadIdx.x; i < (int)(kExtra / 16); i += blockDim.x) {
+            const uint32_t one2 = 0x3F803F80u, one1 = 0x00003F80u;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (i < kTile) v = make_uint4(one2, one1, 0, 0);
+            if (i >= (int)(kSelect / 16) && i < (int)(kSelect / 16) + kTile) v = make_uint4(0, 0, one2, one1);
+            *reinterpret_cast<uint4 *>(select + i * 16) = v;
+        }
+        fence_proxy_async_smem();
+    }
     if (warp == 8) {
         tmem_alloc(smem_addr(&B.tmem), 512);
         tmem_relinquish();
@@ -1054,9 +1088,9 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
     } else {
         regs_down<56>();
         if (st.n > 0) {
-            if (warp == 8) bwd_load<DP, KEYS>(P, B, w, st, mx0, mx1, my0, my1, kept, ring, h);
-            else if (warp == 9) bwd_scores<DP, KEYS>(B, st, kept, ring);
-            else if (warp == 10) bwd_sums<DP, KEYS>(B, st, ring, KEYS ? w.lq : w.lk);
+            if (warp == 8) bwd_load<DP, KEYS>(P, B, w, st, mx0, mx1, my0, my1, kept, ring, stats, h);
+            else if (warp < 11) bwd_scores<DP, KEYS>(B, st, kept, ring, select, stats, warp - 9);
+            else bwd_sums<DP, KEYS>(B, st, ring, KEYS ? w.lq : w.lk);
         }
     }
     __syncwarp();

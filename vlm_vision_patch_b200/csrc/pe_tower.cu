@@ -405,7 +405,7 @@ pe_status pe_attention_last_error(pe_attention *a) {
 
 int64_t pe_attention_workspace(const pe_attention *a, int n_seq, int64_t Nq, int64_t Nk, int backward) {
     if (check_attention(a, n_seq, Nq, Nk) != PE_OK || (backward != 0 && backward != 1)) return -1;
-    return backward ? 2 * (int64_t)a->Hq * Nq * (int64_t)sizeof(float) : 0;
+    return backward ? (int64_t)a->Hq * Nq * (int64_t)sizeof(uint4) : 0;
 }
 
 static AttnParams attention_params(const pe_attention *a, int n_seq, const int32_t *cu_q, int64_t Nq,
@@ -495,8 +495,7 @@ pe_status pe_attention_backward(pe_attention *a, int n_seq, const int32_t *cu_q,
     P.dk = heads_ptr(dk, Nk, a->Hkv);
     P.dv = heads_ptr(dv, Nk, a->Hkv);
     P.lse = const_cast<float *>(lse);
-    P.nlse2 = static_cast<float *>(ws);
-    P.ndelta = P.nlse2 + (int64_t)a->Hq * Nq;
+    P.stat = static_cast<uint4 *>(ws);
     cudaStream_t st = (cudaStream_t)stream;
     CUtensorMap mq, mk, mv, md;
     if (Nq > 0 && (!make_heads_tmap(&mq, q, Nq, a->Hq, D, kStream) || !make_heads_tmap(&md, dout, Nq, a->Hq, D, kStream)))
