@@ -392,6 +392,13 @@ SHAPES = [
     (64, 1, 1, (7,), (2500,), False),
     (80, 1, 1, (2500,), (7,), False),
     (32, 4, 4, tuple([3, 9, 1, 30] * 20), None, False),
+    # few rows on long keys: the key axis divided over blocks, heads packed into a tile
+    (128, 12, 2, (1, 2, 1), (5000, 3000, 77), True),
+    (64, 8, 8, (1, 1), (6000, 4500), False),
+    (80, 6, 2, (20, 3, 0), (9000, 4000, 300), False),
+    (96, 16, 1, (5,), (7001,), True),
+    (128, 2, 1, (1, 40), (0, 9000), False),
+    (72, 5, 1, (9, 25, 11), (3100, 2000, 5000), True),
 ]
 
 
@@ -471,6 +478,21 @@ def test_attention_neighbours_do_not_leak():
     for a, b in zip(clean, dirty):
         assert torch.equal(a[:130], b[:130]) and torch.equal(a[200:n], b[200:n])
         assert (a[n:] == 3.0).all() and (b[n:] == 3.0).all()
+
+
+def test_attention_divided_keys_leave_other_rows():
+    """The joined form (one row on a long key axis) writes rows of sequences only."""
+    D, H, n = 128, 2, 9000
+    q, k, v = normal(47, 4, H, D, dtype=BF), normal(48, n + 50, H, D, dtype=BF), normal(49, n + 50, H, D, dtype=BF)
+    k[n:] = v[n:] = math.nan
+    att = vp.Attention(H, H, D)
+    cq = torch.tensor([1, 2, 3], dtype=torch.int32, device=DEV)      # rows 0 and 3 belong to nobody
+    ck = torch.tensor([0, n, n], dtype=torch.int32, device=DEV)      # the second sequence has no keys
+    assert B.pe_attention_workspace(att.h, 2, 4, n + 50, False) > 0
+    out, lse = att.forward(q, k, v, cq, ck, out=torch.full_like(q, 5.0))
+    R, A = attention_ref(q[1:2], k[:n], v[:n], (1,), (n,), False, D ** -0.5)
+    close(out[1:2], R["out"], A["out"] + U[BF] * R["out"].abs(), "out")
+    assert (out[0] == 5).all() and (out[3] == 5).all() and not out[2].any() and torch.isneginf(lse[:, 2]).all()
 
 
 def test_attention_gradient_against_differences():

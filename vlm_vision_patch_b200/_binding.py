@@ -330,30 +330,36 @@ def pe_last_error(h: int) -> int:
     return int(load().pe_last_error(h))
 
 
-def pe_vision_positions(grid_thw: Sequence[Sequence[int]], merge: int, pos_ptr: Optional[int], cu_ptr: Optional[int],
-                        stream: int) -> None:
-    n = len(grid_thw)
-    _check("pe_vision_positions", load().pe_vision_positions(n, _i32rows(grid_thw) if n else None, merge, pos_ptr,
-                                                             cu_ptr, stream))
+def pe_vision_positions(grid_thw, merge: int, pos_ptr: Optional[int], cu_ptr: Optional[int], stream: int) -> None:
+    """grid_thw: n triples, or their 3 n numbers in one list."""
+    rows = _i32rows(grid_thw)
+    code = load().pe_vision_positions(len(rows) // 3, rows if len(rows) else None, merge, pos_ptr, cu_ptr, stream)
+    if code:
+        raise PEError("pe_vision_positions", code)
 
 
 def pe_rope(q: pe_heads, k: pe_heads, dt: int, N: int, Hq: int, Hk: int, D: int, pos_ptr: int, sections: Sequence[int],
             theta: float, axial: bool, inverse: bool, q_out: pe_heads, k_out: pe_heads, stream: int) -> None:
-    _check("pe_rope", load().pe_rope(q, k, dt, N, Hq, Hk, D, pos_ptr, len(sections), _i32arr(sections), theta,
-                                     int(bool(axial)), int(bool(inverse)), q_out, k_out, stream))
+    code = load().pe_rope(q, k, dt, N, Hq, Hk, D, pos_ptr, len(sections), _i32arr(sections), theta, 1 if axial else 0,
+                          1 if inverse else 0, q_out, k_out, stream)
+    if code:
+        raise PEError("pe_rope", code)
 
 
 def pe_layernorm_forward(x_ptr: int, dt: int, N: int, E: int, gamma: Optional[int], beta: Optional[int], w_dt: int,
                          eps: float, y_ptr: int, mean: Optional[int], rstd: Optional[int], stream: int) -> None:
-    _check("pe_layernorm_forward", load().pe_layernorm_forward(x_ptr, dt, N, E, gamma, beta, w_dt, eps, y_ptr, mean,
-                                                               rstd, stream))
+    code = load().pe_layernorm_forward(x_ptr, dt, N, E, gamma, beta, w_dt, eps, y_ptr, mean, rstd, stream)
+    if code:
+        raise PEError("pe_layernorm_forward", code)
 
 
 def pe_layernorm_backward(dy_ptr: int, x_ptr: int, dt: int, N: int, E: int, gamma: Optional[int], w_dt: int, mean: int,
                           rstd: int, dx_ptr: int, dgamma: Optional[int], dbeta: Optional[int], ws: Optional[int],
                           ws_bytes: int, stream: int) -> None:
-    _check("pe_layernorm_backward", load().pe_layernorm_backward(dy_ptr, x_ptr, dt, N, E, gamma, w_dt, mean, rstd,
-                                                                 dx_ptr, dgamma, dbeta, ws, ws_bytes, stream))
+    code = load().pe_layernorm_backward(dy_ptr, x_ptr, dt, N, E, gamma, w_dt, mean, rstd, dx_ptr, dgamma, dbeta, ws,
+                                        ws_bytes, stream)
+    if code:
+        raise PEError("pe_layernorm_backward", code)
 
 
 def pe_layernorm_backward_workspace(N: int, E: int) -> int:

@@ -208,6 +208,9 @@ struct AttnParams {
     float scale;
     HeadsPtr q, k, v, out, dout, dq, dk, dv;
     float *lse;                   // [Hq, Nq]
+    int pack;                     // query heads of a key head side by side in a tile's rows (forward; 1: none)
+    int splits;                   // parts of the key axis, a block each (forward)
+    float *part_out, *part_lse2;  // [splits, Hq, Nq, D] and [splits, Hq, Nq] (base 2), when splits > 1
     uint4 *stat;                  // [Hq, Nq]: -lse / scale and -dout . out, three bf16 and a 0 each (backward)
     int *err;
 };
@@ -314,6 +317,10 @@ __host__ __device__ constexpr uint32_t idesc_b_mn(int M, int N) { return idesc_b
 // for a product.  The output accumulates in tensor memory too and is rescaled
 // only when a row's maximum has grown by more than 2^8, which keeps P in bf16's
 // range and is rare.
+//
+// With few query rows a sequence (a new token each, say) the heads that share a
+// key head stand side by side in one tile, so its keys are read once for all of
+// them, and several blocks divide the key axis; a second kernel joins their parts.
 
 constexpr int kAttnThreads = 384;             // 168 registers each = 256 * 224 + 128 * 56
 constexpr int kPolyOf4 = 1;                     // of four pairs of exponentials, how many the FMA pipes take
@@ -373,7 +380,7 @@ __device__ __forceinline__ float exp_row(const uint32_t (&s)[C][16], float sl2, 
 
 // Online softmax of one 128-row tile; all 128 threads of its warps.
 template <int DP>
-__device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, const Work &w, int tile, int n_kv, int n_other, int h) {
+__device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, const Work &w, int tile, int n_kv, int n_other, int kb, int h) {
     using S = FwdShape<DP>;
     constexpr int C = S::KT / 16;
     volatile int *abort = &B.abort;
@@ -381,8 +388,13 @@ __device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, con
     const uint32_t lanes = B.tmem + ((uint32_t)(warp & 3) << 21);  // 32 lanes a warp, in bits 16..
     const uint32_t ts = lanes + S::kColS + tile * S::KT, tp = lanes + S::kColP + tile * (S::KT / 2);
     const uint32_t to = lanes + S::kColO + tile * DP;
-    const int i = w.row + tile * kTile + (warp & 3) * 32 + lane;   // row within the sequence
-    const int limit = keys_seen(P, w, i);
+    const int r = (warp & 3) * 32 + lane, rows = kTile / P.pack;   // place in the tile, query rows of a tile
+    const int i = w.row + tile * rows + r / P.pack;                // row within the sequence
+    const int head = P.pack > 1 ? h * P.pack + r % P.pack : h;
+    // Rows of no use (behind the sequence, or of no head) hold what lies there: they
+    // take no part in the warp's votes, or a result's last bits would depend on them.
+    const bool mine = i < w.lq && r < rows * P.pack;
+    const int limit = mine ? keys_seen(P, w, i) - kb : INT32_MAX;  // of this block's keys
     const float sl2 = P.scale * kLog2e;
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n_kv; ++j) {
@@ -412,7 +424,7 @@ __device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, con
                 for (int k = 0; k < 4; ++k)
                     mx4[k] = max3_nan(mx4[k], __uint_as_float(s[c][e + 2 * k]), __uint_as_float(s[c][e + 2 * k + 1]));
         const float mx = max3_nan(max3_nan(mx4[0], mx4[1], mx4[2]), mx4[3], mx4[3]);
-        if (__any_sync(0xffffffffu, (mx - m) * sl2 > 8.0f)) {
+        if (__any_sync(0xffffffffu, mine && (mx - m) * sl2 > 8.0f)) {
             const float f = m == -INFINITY ? 0.f : ex2((m - mx) * sl2);
             l *= f;
             m = mx;
@@ -454,46 +466,88 @@ __device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, con
         if (!warp_wait(&B.pv_done[tile], (n_kv - 1) & 1, abort)) return;
         tc_fence_after();
     }
-    const bool mine = i < w.lq;
     const float inv = 1.0f / l;
-    __nv_bfloat16 *out = P.out.at(w.q0 + i, h);
+    const int64_t at = (int64_t)head * P.Nq + w.q0 + i, part = (int64_t)blockIdx.z * P.Hq * P.Nq + at;
+    __nv_bfloat16 *out = P.out.at(w.q0 + i, head);
 #pragma unroll
     for (int c = 0; c < DP / 16; ++c) {
-        uint32_t o[16] = {0};
+        uint32_t o[1][16] = {{0}};
         if (n_kv > 0) {
-            tmem_ld_x16(to + 16 * c, o);
-            tmem_ld_wait();
+            tmem_ld_x16(to + 16 * c, o[0]);
+            tmem_ld_wait_for(o);
         }
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            uint32_t pk[4];
+            if (!mine || 16 * c + 8 * g >= P.D) continue;
+            float v[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float a = __uint_as_float(o[8 * g + 2 * e]) * inv, b = __uint_as_float(o[8 * g + 2 * e + 1]) * inv;
-                pk[e] = limit > 0 ? pack_bf16x2(a, b) : 0u;
+            for (int e = 0; e < 8; ++e) v[e] = limit > 0 ? __uint_as_float(o[0][8 * g + e]) * inv : 0.f;
+            if (P.splits > 1) {
+                float4 *dst = reinterpret_cast<float4 *>(P.part_out + part * P.D + 16 * c + 8 * g);
+                dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+                st_global_v4(out + 16 * c + 8 * g, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
             }
-            if (mine && 16 * c + 8 * g < P.D) st_global_v4(out + 16 * c + 8 * g, pk[0], pk[1], pk[2], pk[3]);
         }
     }
-    if (mine && P.lse)
-        P.lse[(int64_t)h * P.Nq + w.q0 + i] = limit > 0 ? m * P.scale + logf(l) : -INFINITY;
+    if (!mine) return;
+    if (P.splits > 1) P.part_lse2[part] = limit > 0 ? m * sl2 + log2f(l) : -INFINITY;
+    else if (P.lse) P.lse[at] = limit > 0 ? m * P.scale + logf(l) : -INFINITY;
+}
+
+// Joins the parts of a row and head (one warp each): out = sum_z w_z out_z / sum_z
+// w_z with w_z = 2^(lse2_z - max).
+__global__ void __launch_bounds__(256) pe_attn_join_kernel(const __grid_constant__ AttnParams P) {
+    const int lane = threadIdx.x & 31;
+    const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);          // [Hq, Nq]
+    if (at >= (int64_t)P.Hq * P.Nq) return;
+    const int h = (int)(at / P.Nq), r = (int)(at - (int64_t)h * P.Nq);
+    int lo = -1, hi = P.n_seq - 1;                        // the last sequence that begins at or before r
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (boundary(P.cu_q, mid, P.Nq) <= r) lo = mid; else hi = mid - 1;
+    }
+    if (lo < 0 || r >= boundary(P.cu_q, lo + 1, P.Nq)) return;                // a row of no sequence
+    const int64_t step = (int64_t)P.Hq * P.Nq;
+    float top = -INFINITY;
+    for (int z = 0; z < P.splits; ++z) top = fmaxf(top, P.part_lse2[z * step + at]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int z = 0; z < P.splits; ++z) {
+        const float l = P.part_lse2[z * step + at];
+        if (l == -INFINITY) continue;                     // saw no key
+        const float w = ex2(l - top);
+        sum += w;
+        if (4 * lane < P.D) {
+            const float4 v = *reinterpret_cast<const float4 *>(P.part_out + (z * step + at) * P.D + 4 * lane);
+            o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    if (4 * lane < P.D)
+        *reinterpret_cast<uint2 *>(P.out.at(r, h) + 4 * lane) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (lane == 0 && P.lse) P.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) / kLog2e;
 }
 
 // Loads (one warp): Q, then K0 K1 V0 K2 V1 ... (the order of use) through one ring.
 template <int DP>
 __device__ __forceinline__ void fwd_load(const AttnParams &P, FwdBars &B, const Work &w, const CUtensorMap &mq,
                                          const CUtensorMap &mk, const CUtensorMap &mv, uint8_t *sq, uint8_t *ring, bool two,
-                                         int n_max, int h, int hk) {
+                                         int n_max, int kb, int h, int hk) {
     using S = FwdShape<DP>;
     constexpr int KT = S::KT;
     volatile int *abort = &B.abort;
     const int lane = threadIdx.x & 31;
     if (n_max > 0 && lane == 0) {
-        mbar_arrive_expect_tx(smem_addr(&B.qfull), (two ? 2 : 1) * S::kQ);
+        const int rows = kTile / P.pack;                    // the box of mq: rows x pack heads
+        mbar_arrive_expect_tx(smem_addr(&B.qfull), (two ? 2 : 1) * S::kC * rows * P.pack * 128);
         for (int t = 0; t < (two ? 2 : 1); ++t)
             for (int c = 0; c < S::kC; ++c)
-                tma_load_3d(smem_addr(sq + t * S::kQ + c * kChunkBytes), &mq, smem_addr(&B.qfull), 64 * c, h,
-                            w.q0 + w.row + t * kTile);
+                tma_load_3d(smem_addr(sq + t * S::kQ + c * kChunkBytes), &mq, smem_addr(&B.qfull), 64 * c, h * P.pack,
+                            w.q0 + w.row + t * rows);
     }
     int f = 0;
     bool ok = true;
@@ -504,14 +558,14 @@ __device__ __forceinline__ void fwd_load(const AttnParams &P, FwdBars &B, const 
         ok = warp_wait(&B.empty[slot], ((f / S::kStages) & 1) ^ 1, abort);
         if (!ok) break;
         uint8_t *dst = ring + slot * S::kKv;
-        const int valid = min(w.lk - j * KT, KT);
+        const int valid = min(w.lk - kb - j * KT, KT);
         const bool clean = is_v && valid < KT;          // the last tile of V: zeros behind the sequence
         uint64_t *bar = clean ? &B.tail : &B.full[slot];
         if (lane == 0) {
             mbar_arrive_expect_tx(smem_addr(bar), S::kKv);
             for (int c = 0; c < S::kC; ++c)
                 tma_load_3d(smem_addr(dst + c * S::kChunk), is_v ? &mv : &mk, smem_addr(bar), 64 * c, hk,
-                            w.k0 + j * KT);
+                            w.k0 + kb + j * KT);
         }
         __syncwarp();
         if (clean) {
@@ -537,7 +591,8 @@ __device__ __forceinline__ void fwd_load(const AttnParams &P, FwdBars &B, const 
 // warp shares its instruction queue with the exponentials, and one warp for both
 // tiles spent longer queueing than the tensor cores working.
 template <int DP>
-__device__ __forceinline__ void fwd_mma(FwdBars &B, const Work &w, uint8_t *sq, uint8_t *ring, int t, int n, int n_max) {
+__device__ __forceinline__ void fwd_mma(FwdBars &B, const Work &w, uint8_t *sq, uint8_t *ring, int t, int n, int n_max,
+                                        int kb) {
     using S = FwdShape<DP>;
     constexpr int KT = S::KT;
     constexpr uint32_t kIdS = idesc_bf16_f32(kTile, KT), kIdO = idesc_b_mn(kTile, DP);
@@ -584,7 +639,7 @@ __device__ __forceinline__ void fwd_mma(FwdBars &B, const Work &w, uint8_t *sq, 
         if (!ok) break;
         tc_fence_after();
         if (j < n) {
-            const int steps = (min(w.lk - j * KT, KT) + 15) / 16;
+            const int steps = (min(w.lk - kb - j * KT, KT) + 15) / 16;
             const uint32_t b = d_v + slot_of(fv);
             if (one) {
                 mma_ts(to, tp, b, kDescHi, kIdO, j > 0);
@@ -605,7 +660,7 @@ __device__ __forceinline__ void fwd_mma(FwdBars &B, const Work &w, uint8_t *sq, 
     if (!ok) drain_mmas(one, &B.drain[t]);
 }
 
-// mk, mv: boxes of kKeys rows; mq: of 128.
+// mk, mv: boxes of kKeys rows; mq: of 128 / pack rows and pack heads.
 template <int DP>
 __global__ void __launch_bounds__(kAttnThreads, 1)
 pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -616,13 +671,13 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     __shared__ FwdBars B;
     uint8_t *sq = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023), *ring = sq + 2 * S::kQ;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.y, hk = h / (P.Hq / P.Hkv);
+    const int h = blockIdx.y, hk = P.pack > 1 ? h : h / (P.Hq / P.Hkv), rows = kTile / P.pack;
     if (warp == 9) {
-        const Work w = find_work(P, false, blockIdx.x, 2 * kTile);
+        const Work w = find_work(P, false, blockIdx.x, 2 * rows);
         if (lane == 0) {
             B.w = w;
             B.abort = 0;
-            const int tiles = w.lq - w.row > kTile ? 2 : 1;  // each gives a slot back
+            const int tiles = w.lq - w.row > rows ? 2 : 1;  // each gives a slot back
             for (int i = 0; i < S::kStages; ++i) mbar_init(smem_addr(&B.full[i]), 1), mbar_init(smem_addr(&B.empty[i]), tiles);
             mbar_init(smem_addr(&B.tail), 1);
             mbar_init(smem_addr(&B.qfull), 1);
@@ -650,20 +705,24 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // key tiles that each query tile meets (the second tile may be missing)
+    // key tiles that each query tile meets (the second tile may be missing) ...
     auto tiles_of = [&](int t) {
-        const int last = min(w.row + (t + 1) * kTile, w.lq) - 1;
-        return w.lq - w.row > t * kTile ? (keys_seen(P, w, last) + KT - 1) / KT : 0;
+        const int last = min(w.row + (t + 1) * rows, w.lq) - 1;
+        return w.lq - w.row > t * rows ? (keys_seen(P, w, last) + KT - 1) / KT : 0;
     };
-    const bool two = w.lq - w.row > kTile;
-    const int n0 = tiles_of(0), n1 = tiles_of(1), n_max = max(n0, n1);
+    const bool two = w.lq - w.row > rows;
+    const int all0 = tiles_of(0), all1 = tiles_of(1), all = max(all0, all1);
+    // ... and this block's part of them, from key kb on
+    const int from = (int)((int64_t)all * blockIdx.z / P.splits), to = (int)((int64_t)all * (blockIdx.z + 1) / P.splits);
+    const int kb = from * KT, n_max = to - from;
+    const int n0 = min(max(all0 - from, 0), n_max), n1 = min(max(all1 - from, 0), n_max);
     if (warp < 8) {
         regs_up<224>();
-        if (warp < 4 || two) fwd_softmax<DP>(P, B, w, warp >> 2, warp < 4 ? n0 : n1, warp < 4 ? n1 : n0, h);
+        if (warp < 4 || two) fwd_softmax<DP>(P, B, w, warp >> 2, warp < 4 ? n0 : n1, warp < 4 ? n1 : n0, kb, h);
     } else {
         regs_down<56>();
-        if (warp == 8) fwd_load<DP>(P, B, w, mq, mk, mv, sq, ring, two, n_max, h, hk);
-        else if (warp < (two ? 11 : 10)) fwd_mma<DP>(B, w, sq, ring, warp - 9, warp == 9 ? n0 : n1, n_max);
+        if (warp == 8) fwd_load<DP>(P, B, w, mq, mk, mv, sq, ring, two, n_max, kb, h, hk);
+        else if (warp < (two ? 11 : 10)) fwd_mma<DP>(B, w, sq, ring, warp - 9, warp == 9 ? n0 : n1, n_max, kb);
     }
     __syncwarp();
     tc_fence_before();

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -31,12 +32,14 @@ bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 
 size_t size_of(pe_dtype dt) { return dt == PE_F32 ? 4 : 2; }
 
-// Streaming multiprocessors of the current device.
+// Streaming multiprocessors of the current device (asked for once per device).
 int current_sms() {
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
@@ -143,15 +146,16 @@ HeadsPtr heads_ptr(const pe_heads &t, int64_t rows, int heads) {
     return {static_cast<__nv_bfloat16 *>(t.ptr), rows > 1 ? t.row_stride : 0, heads > 1 ? t.head_stride : 0};
 }
 
-// [rows, heads, D] bf16 in boxes of `box_rows` rows of one head and 64 elements, 128-byte
+// [rows, heads, D] bf16 in boxes of `box_rows` rows, `box_heads` heads and 64 elements, 128-byte
 // swizzle; what lies outside reads as zero.
-bool make_heads_tmap(CUtensorMap *m, const pe_heads &t, int64_t rows, int heads, int D, uint32_t box_rows) {
+bool make_heads_tmap(CUtensorMap *m, const pe_heads &t, int64_t rows, int heads, int D, uint32_t box_rows,
+                     uint32_t box_heads = 1) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const int64_t row = rows > 1 ? t.row_stride : (int64_t)heads * D, head = heads > 1 ? t.head_stride : D;
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
     cuuint64_t strides[2] = {(cuuint64_t)head * 2, (cuuint64_t)row * 2};
-    cuuint32_t box[3] = {64, 1, box_rows}, estr[3] = {1, 1, 1};
+    cuuint32_t box[3] = {64, box_heads, box_rows}, estr[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -169,12 +173,18 @@ auto with_head_size(int D, F &&f) {
 
 // Prepares an attention kernel of 384 threads whose warpgroups divide the
 // registers anew (setmaxnreg): more than it was launched with would be waited for
-// without end, so a build that gave it fewer is refused.
+// without end, so a build that gave it fewer is refused.  Once per kernel and
+// device (`done`: a bit each); a second thread that does it again does no harm.
 template <class Kernel>
-bool ready_to_launch(Kernel kern, size_t smem) {
+bool ready_to_launch(Kernel kern, size_t smem, int dev, std::atomic<uint64_t> &done) {
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
     cudaFuncAttributes at;
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess &&
-           cudaFuncGetAttributes(&at, kern) == cudaSuccess && at.numRegs * kAttnThreads >= 256 * 224 + 128 * 56;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+        cudaFuncGetAttributes(&at, kern) != cudaSuccess || at.numRegs * kAttnThreads < 256 * 224 + 128 * 56)
+        return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
 }
 
 // Tiles of `rows` rows that n rows in n_seq sequences can make, at most.
@@ -185,6 +195,29 @@ pe_status check_attention(const pe_attention *a, int n_seq, int64_t Nq, int64_t 
     if (!a || n_seq < 0 || Nq < 0 || Nk < 0) return PE_ERR_INVALID_ARG;
     if (Nq > INT32_MAX - 256 || Nk > INT32_MAX - 256 || n_seq > (1 << 24)) return PE_ERR_UNSUPPORTED;
     return PE_OK;
+}
+
+// How a forward call lays its rows and keys out over blocks, from the sizes alone.
+struct FwdPlan {
+    int pack, splits;
+    unsigned blocks, rows;       // blocks of one head and split; heads or, packed, key heads
+};
+
+FwdPlan plan_forward(const pe_attention *a, int n_seq, int64_t Nq, int64_t Nk) {
+    const int share = a->Hq / a->Hkv;
+    FwdPlan p;
+    // an average sequence's rows of all heads that share a key head fit one tile
+    p.pack = share > 1 && share <= kTile && Nq * share <= (int64_t)kTile * n_seq ? share : 1;
+    p.blocks = max_tiles(Nq, n_seq, 2 * (kTile / p.pack));
+    p.rows = (unsigned)(p.pack > 1 ? a->Hkv : a->Hq);
+    // With blocks for less than a quarter of the SMs the key axis is divided until
+    // there are two a SM, but into no less than 4 tiles of an average sequence.
+    const int64_t blocks = (int64_t)std::min<int64_t>(p.blocks, Nq) * p.rows;
+    const int64_t tiles = Nk / n_seq / 128;
+    p.splits = 1;
+    if (blocks * 4 <= a->num_sms)
+        p.splits = (int)std::max<int64_t>(1, std::min(2 * a->num_sms / blocks, std::min<int64_t>(tiles / 4, 64)));
+    return p;
 }
 
 }  // namespace
@@ -405,7 +438,10 @@ pe_status pe_attention_last_error(pe_attention *a) {
 
 int64_t pe_attention_workspace(const pe_attention *a, int n_seq, int64_t Nq, int64_t Nk, int backward) {
     if (check_attention(a, n_seq, Nq, Nk) != PE_OK || (backward != 0 && backward != 1)) return -1;
-    return backward ? (int64_t)a->Hq * Nq * (int64_t)sizeof(uint4) : 0;
+    if (backward) return (int64_t)a->Hq * Nq * (int64_t)sizeof(uint4);
+    if (n_seq == 0 || Nq == 0) return 0;
+    const int splits = plan_forward(a, n_seq, Nq, Nk).splits;
+    return splits > 1 ? (int64_t)splits * a->Hq * Nq * (a->D + 1) * (int64_t)sizeof(float) : 0;
 }
 
 static AttnParams attention_params(const pe_attention *a, int n_seq, const int32_t *cu_q, int64_t Nq,
@@ -447,17 +483,32 @@ pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, 
     P.k = heads_ptr(k, Nk, a->Hkv);
     P.v = heads_ptr(v, Nk, a->Hkv);
     P.lse = lse;
+    const FwdPlan plan = plan_forward(a, n_seq, Nq, Nk);
+    P.pack = plan.pack;
+    P.splits = plan.splits;
+    if (plan.splits > 1) {
+        if (!ws) return PE_ERR_INVALID_ARG;
+        if (!aligned16(ws)) return PE_ERR_ALIGN;
+        if (ws_bytes < pe_attention_workspace(a, n_seq, Nq, Nk, 0)) return PE_ERR_SHAPE;
+        P.part_out = static_cast<float *>(ws);
+        P.part_lse2 = P.part_out + (int64_t)plan.splits * a->Hq * Nq * D;
+    }
+    cudaStream_t st = (cudaStream_t)stream;
     return with_head_size(D, [&](auto dp) {
         using S = FwdShape<decltype(dp)::value>;
         CUtensorMap mq, mk, mv;
-        if (!make_heads_tmap(&mq, q, Nq, a->Hq, D, kTile)) return PE_ERR_CUDA;
+        if (!make_heads_tmap(&mq, q, Nq, a->Hq, D, kTile / plan.pack, plan.pack)) return PE_ERR_CUDA;
         mk = mv = mq;                                       // without keys their maps are not read
         if (Nk > 0 && (!make_heads_tmap(&mk, k, Nk, a->Hkv, D, S::KT) || !make_heads_tmap(&mv, v, Nk, a->Hkv, D, S::KT)))
             return PE_ERR_CUDA;
         auto kern = pe_attn_fwd_kernel<decltype(dp)::value>;
-        if (!ready_to_launch(kern, S::kSmem)) return PE_ERR_CUDA;
-        const dim3 grid(max_tiles(Nq, n_seq, 2 * kTile), (unsigned)a->Hq);
-        kern<<<grid, kAttnThreads, S::kSmem, (cudaStream_t)stream>>>(mq, mk, mv, P);
+        static std::atomic<uint64_t> done{0};
+        if (!ready_to_launch(kern, S::kSmem, a->dev, done)) return PE_ERR_CUDA;
+        kern<<<dim3(plan.blocks, plan.rows, (unsigned)plan.splits), kAttnThreads, S::kSmem, st>>>(mq, mk, mv, P);
+        if (plan.splits > 1) {
+            if (cudaGetLastError() != cudaSuccess) return PE_ERR_CUDA;
+            pe_attn_join_kernel<<<(unsigned)(((int64_t)a->Hq * Nq + 7) / 8), 256, 0, st>>>(P);
+        }
         return finish(cudaGetLastError());
     });
 }
@@ -509,8 +560,10 @@ pe_status pe_attention_backward(pe_attention *a, int n_seq, const int32_t *cu_q,
         constexpr int DP = decltype(dp)::value;
         auto dq_kern = pe_attn_bwd_kernel<DP, false>;
         auto dkv_kern = pe_attn_bwd_kernel<DP, true>;
-        for (auto kern : {dq_kern, dkv_kern})
-            if (!ready_to_launch(kern, kBwdSmem<DP>)) return PE_ERR_CUDA;
+        static std::atomic<uint64_t> dq_done{0}, dkv_done{0};
+        if (!ready_to_launch(dq_kern, kBwdSmem<DP>, a->dev, dq_done) ||
+            !ready_to_launch(dkv_kern, kBwdSmem<DP>, a->dev, dkv_done))
+            return PE_ERR_CUDA;
         if (Nq > 0) {
             const dim3 grid(max_tiles(Nq, n_seq, kTile), (unsigned)a->Hq);
             dq_kern<<<grid, kAttnThreads, kBwdSmem<DP>, st>>>(mq, md, mk, mv, P);

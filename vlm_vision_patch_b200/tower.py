@@ -11,7 +11,6 @@ here records an autograd graph: the gradient calls are functions of their own.
 """
 from __future__ import annotations
 
-import contextlib
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -21,42 +20,43 @@ from . import _dt, _need, _raw_stream
 
 __all__ = ["vision_positions", "rope", "layer_norm", "layer_norm_backward", "Attention"]
 
-_HERE = contextlib.nullcontext()
+_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+_NONE = B.pe_heads(None, 0, 0)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _elsewhere(device: int, stream) -> bool:
+    """Whether a call has to enter another device or stream first (`_on`)."""
+    return stream is not None or (device >= 0 and device != _current_device())
 
 
 def _on(device: int, stream):
-    """(context in which `device` and `stream` are current, raw stream handle)."""
+    """Context in which `device` and `stream` (None: the device's current one) are current."""
+    if device < 0:
+        raise ValueError("the tensors must be CUDA tensors")
     if stream is None:
-        if torch.cuda.current_device() == device:
-            return _HERE, _raw(device)
-        return torch.cuda.device(device), _raw(device)
+        return torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
                   else torch.cuda.default_stream(device))
     if stream.device.index != device:
         raise ValueError(f"stream is on cuda:{stream.device.index}, the tensors on cuda:{device}")
-    return torch.cuda.stream(stream), stream.cuda_stream
+    return torch.cuda.stream(stream)
 
 
 def _raw(device: int) -> int:
     if _raw_stream is not None:
-        return int(_raw_stream(device))
+        return _raw_stream(device)
     return torch.cuda.current_stream(device).cuda_stream
 
 
-def _device(t: torch.Tensor, name: str) -> int:
-    d = t.get_device()
-    if d < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return d
-
-
-def _dense(t: torch.Tensor, name: str, device: int, shape: Optional[Sequence[int]] = None,
-           dtype: Optional[torch.dtype] = None) -> int:
+def _dense(t: torch.Tensor, name: str, device: int, shape=None, dtype: Optional[torch.dtype] = None) -> int:
     """Data pointer of a contiguous tensor on `device`."""
+    if device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}; expected cuda:{device}")
-    if shape is not None:
+    if shape is not None and t.shape != shape:
         _need(t, shape, name)
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}; expected {dtype}")
@@ -65,17 +65,19 @@ def _dense(t: torch.Tensor, name: str, device: int, shape: Optional[Sequence[int
     return t.data_ptr()
 
 
-def _heads(t: torch.Tensor, name: str, device: int, dtype: torch.dtype, shape: Sequence[int]) -> B.pe_heads:
+def _heads(t: torch.Tensor, name: str, device: int, dtype: torch.dtype, shape) -> B.pe_heads:
     """A [rows, heads, D] tensor whose last axis is contiguous."""
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}; expected cuda:{device}")
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{name} is on {t.device}; expected cuda:{device}" if device >= 0
+                         else f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}; expected {dtype}")
-    _need(t, shape, name)
-    s = t.stride()
-    if s[2] != 1 and t.shape[2] > 1 and t.numel():
+    if t.shape != shape:
+        _need(t, shape, name)
+    row, head, one = t.stride()
+    if one != 1 and shape[2] > 1 and t.numel():
         raise ValueError(f"the last axis of {name} must be contiguous")
-    return B.pe_heads(t.data_ptr(), s[0], s[1])
+    return B.pe_heads(t.data_ptr(), row, head)
 
 
 def vision_positions(grid_thw: Sequence[Sequence[int]], merge: int = 2, device=None,
@@ -84,22 +86,28 @@ def vision_positions(grid_thw: Sequence[Sequence[int]], merge: int = 2, device=N
     pos is int32 [3, N], the (t, h, w) of every row; cu_seqlens is int32
     [frames + 1], the first row of every frame and N.  `device` defaults to the
     current CUDA device."""
+    grids, n, frames = [], 0, 0
     for g in grid_thw:
         if len(g) != 3:
             raise ValueError("every grid_thw entry must be (t, h, w)")
-    grids = [int(v) for g in grid_thw for v in g]
-    n = sum(grids[i] * grids[i + 1] * grids[i + 2] for i in range(0, len(grids), 3))
-    if any(v < 1 for v in grids) or n >= 2 ** 31:
-        raise ValueError("grid_thw entries must be positive and their patches fewer than 2^31")
-    dev = torch.cuda.current_device() if device is None else torch.device(device).index
+        t, h, w = int(g[0]), int(g[1]), int(g[2])
+        if t < 1 or h < 1 or w < 1:
+            raise ValueError("grid_thw entries must be positive")
+        grids += (t, h, w)
+        n += t * h * w
+        frames += t
+    if n >= 2 ** 31:
+        raise ValueError("the grids hold 2^31 patches or more")
+    dev = None if device is None else torch.device(device).index
     if dev is None:
-        dev = torch.cuda.current_device()
-    ctx, st = _on(dev, stream)
-    with ctx:
-        pos = torch.empty((3, n), dtype=torch.int32, device=dev)
-        cu = torch.empty(sum(grids[0::3]) + 1, dtype=torch.int32, device=dev)
-        B.pe_vision_positions([grids[i:i + 3] for i in range(0, len(grids), 3)], merge, pos.data_ptr(), cu.data_ptr(),
-                              st)
+        dev = _current_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return vision_positions(grid_thw, merge, dev)
+    where = torch.device("cuda", dev)
+    pos = torch.empty((3, n), dtype=_I32, device=where)
+    cu = torch.empty(frames + 1, dtype=_I32, device=where)
+    B.pe_vision_positions(grids, merge, pos.data_ptr(), cu.data_ptr(), _raw(dev))
     return pos, cu
 
 
@@ -115,40 +123,44 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, sections
     (D/4, D/4) on pos[1:] of `vision_positions`; M-RoPE sections (16, 24, 24).
     ``inverse`` turns back, which is the gradient.  Pass ``out_q=q`` (and
     ``out_k=k``) to work in place."""
-    dev = _device(q, "q")
+    dev = q.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return rope(q, k, pos, sections, theta, axial, inverse, out_q, out_k)
     if q.dim() != 3 or (k is not None and k.dim() != 3):
         raise ValueError("q and k must be [N, heads, D]")
-    n, hq, d = q.shape
-    hk = 0 if k is None else k.shape[1]
     if pos.dim() != 2 or pos.shape[0] != len(sections):
         raise ValueError(f"pos must be [{len(sections)}, N]; got {tuple(pos.shape)}")
-    pos_ptr = _dense(pos, "pos", dev, (len(sections), n), torch.int32)
-    dt = _dt(q.dtype)
-    ctx, st = _on(dev, stream)
-    with ctx:
-        if out_q is None:
-            out_q = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
-        none = B.pe_heads(None, 0, 0)
-        qs, qo = _heads(q, "q", dev, q.dtype, (n, hq, d)), _heads(out_q, "out_q", dev, q.dtype, (n, hq, d))
-        ks = ko = none
-        if k is not None:
-            if out_k is None:
-                out_k = torch.empty((n, hk, d), dtype=q.dtype, device=q.device)
-            ks, ko = _heads(k, "k", dev, q.dtype, (n, hk, d)), _heads(out_k, "out_k", dev, q.dtype, (n, hk, d))
-        B.pe_rope(qs, ks, dt, n, hq, hk, d, pos_ptr, sections, float(theta), axial, inverse, qo, ko, st)
+    dtype, shape = q.dtype, q.shape
+    n, hq, d = shape
+    dt = _dt(dtype)
+    pos_ptr = _dense(pos, "pos", dev, (len(sections), n), _I32)
+    qs = _heads(q, "q", dev, dtype, shape)
+    if out_q is None:
+        out_q = q.new_empty(shape)
+    qo = _heads(out_q, "out_q", dev, dtype, shape)
+    hk, ks, ko = 0, _NONE, _NONE
+    if k is not None:
+        hk = k.shape[1]
+        k_shape = (n, hk, d)
+        ks = _heads(k, "k", dev, dtype, k_shape)
+        if out_k is None:
+            out_k = k.new_empty(k_shape)
+        ko = _heads(out_k, "out_k", dev, dtype, k_shape)
+    B.pe_rope(qs, ks, dt, n, hq, hk, d, pos_ptr, sections, theta, axial, inverse, qo, ko, _raw(dev))
     return out_q, out_k if k is not None else None
 
 
 def _weights(dev: int, E: int, **weights) -> Tuple[list, int]:
     """Pointers of the optional [E] weights, which share one dtype."""
-    ptrs, dts = [], set()
+    ptrs, dtype = [], None
     for name, w in weights.items():
         ptrs.append(None if w is None else _dense(w, name, dev, (E,)))
         if w is not None:
-            dts.add(w.dtype)
-    if len(dts) > 1:
-        raise TypeError("the weights must share one dtype")
-    return ptrs, _dt(dts.pop()) if dts else B.PE_F32
+            if dtype is not None and w.dtype != dtype:
+                raise TypeError("the weights must share one dtype")
+            dtype = w.dtype
+    return ptrs, B.PE_F32 if dtype is None else _dt(dtype)
 
 
 def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
@@ -156,21 +168,24 @@ def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Opti
     """Layer norm over the last axis of a contiguous x [..., E]; gamma and beta
     are [E] or None.  With ``stats`` returns (y, mean, rstd), the fp32
     statistics of every row that `layer_norm_backward` takes.  ``out`` may be x."""
-    dev = _device(x, "x")
+    dev = x.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return layer_norm(x, gamma, beta, eps, out, stats)
     if x.dim() < 1:
         raise ValueError("x must be [..., E]")
-    E, lead = x.shape[-1], x.shape[:-1]
+    shape = x.shape
+    E, lead = shape[-1], shape[:-1]
     xp, dt = _dense(x, "x", dev), _dt(x.dtype)
     (g, b), w_dt = _weights(dev, E, gamma=gamma, beta=beta)
-    ctx, st = _on(dev, stream)
-    with ctx:
-        if out is None:
-            out = torch.empty_like(x)
-        op = _dense(out, "out", dev, x.shape, x.dtype)
-        mean = torch.empty(lead, dtype=torch.float32, device=x.device) if stats else None
-        rstd = torch.empty_like(mean) if stats else None
-        B.pe_layernorm_forward(xp, dt, lead.numel(), E, g, b, w_dt, eps, op, mean.data_ptr() if stats else None,
-                               rstd.data_ptr() if stats else None, st)
+    if out is None:
+        out = torch.empty_like(x)
+    op = _dense(out, "out", dev, shape, x.dtype)
+    mean = rstd = mp = rp = None
+    if stats:
+        mean, rstd = x.new_empty(lead, dtype=_F32), x.new_empty(lead, dtype=_F32)
+        mp, rp = mean.data_ptr(), rstd.data_ptr()
+    B.pe_layernorm_forward(xp, dt, lead.numel(), E, g, b, w_dt, eps, op, mp, rp, _raw(dev))
     return (out, mean, rstd) if stats else out
 
 
@@ -180,33 +195,35 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch
     """(dx, dgamma, dbeta) of `layer_norm` for the gradient dy of its output; the
     weight's gradients are None with ``weight_grads=False``.  They have gamma's
     dtype (``weight_dtype``, or fp32, without a gamma).  ``out`` may be dy or x."""
-    dev = _device(x, "x")
-    E, lead = x.shape[-1], x.shape[:-1]
+    dev = x.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return layer_norm_backward(dy, x, gamma, mean, rstd, weight_grads, out, weight_dtype)
+    if x.dim() < 1:
+        raise ValueError("x must be [..., E]")
+    shape = x.shape
+    E, lead = shape[-1], shape[:-1]
+    n = lead.numel()
     xp, dt = _dense(x, "x", dev), _dt(x.dtype)
-    dp = _dense(dy, "dy", dev, x.shape, x.dtype)
-    mp, rp = _dense(mean, "mean", dev, lead, torch.float32), _dense(rstd, "rstd", dev, lead, torch.float32)
+    dp = _dense(dy, "dy", dev, shape, x.dtype)
+    mp, rp = _dense(mean, "mean", dev, lead, _F32), _dense(rstd, "rstd", dev, lead, _F32)
     (g,), w_dt = _weights(dev, E, gamma=gamma)
     if weight_dtype is not None:
         if gamma is not None and weight_dtype != gamma.dtype:
             raise TypeError("weight_dtype must be gamma's dtype")
         w_dt = _dt(weight_dtype)
-    ctx, st = _on(dev, stream)
-    with ctx:
-        if out is None:
-            out = torch.empty_like(x)
-        op = _dense(out, "out", dev, x.shape, x.dtype)
-        dgamma = dbeta = ws = None
-        nbytes = 0
-        if weight_grads:
-            w_type = torch.float32 if w_dt == B.PE_F32 else torch.bfloat16
-            dgamma = torch.empty(E, dtype=w_type, device=x.device)
-            dbeta = torch.empty_like(dgamma)
-            nbytes = max(B.pe_layernorm_backward_workspace(lead.numel(), E), 0)
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-        B.pe_layernorm_backward(dp, xp, dt, lead.numel(), E, g, w_dt, mp, rp, op,
-                                dgamma.data_ptr() if weight_grads else None,
-                                dbeta.data_ptr() if weight_grads else None, ws.data_ptr() if weight_grads else None,
-                                nbytes, st)
+    if out is None:
+        out = torch.empty_like(x)
+    op = _dense(out, "out", dev, shape, x.dtype)
+    dgamma = dbeta = gp = bp = ws = None
+    nbytes = 0
+    if weight_grads:
+        dgamma = x.new_empty(E, dtype=_F32 if w_dt == B.PE_F32 else _BF16)
+        dbeta = torch.empty_like(dgamma)
+        nbytes = B.pe_layernorm_backward_workspace(n, E)
+        scratch = x.new_empty(max(nbytes, 0), dtype=torch.uint8)
+        gp, bp, ws = dgamma.data_ptr(), dbeta.data_ptr(), scratch.data_ptr()
+    B.pe_layernorm_backward(dp, xp, dt, n, E, g, w_dt, mp, rp, op, gp, bp, ws, max(nbytes, 0), _raw(dev))
     return out, dgamma, dbeta
 
 
@@ -227,22 +244,28 @@ class Attention:
         self.dev = torch.cuda.current_device()   # the device pe_attention_create bound the handle to
 
     def _cu(self, cu_q, cu_k):
-        for t, name in ((cu_q, "cu_q"), (cu_k, "cu_k")):
-            if t.dim() != 1 or t.shape[0] < 1:
-                raise ValueError(f"{name} must be [n_seq + 1]; got {tuple(t.shape)}")
-        if cu_q.shape != cu_k.shape:
-            raise ValueError(f"cu_q {tuple(cu_q.shape)} and cu_k {tuple(cu_k.shape)} hold different sequence counts")
-        return (cu_q.shape[0] - 1, _dense(cu_q, "cu_q", self.dev, dtype=torch.int32),
-                _dense(cu_k, "cu_k", self.dev, dtype=torch.int32))
+        n = cu_q.shape
+        if len(n) != 1 or n[0] < 1:
+            raise ValueError(f"cu_q must be [n_seq + 1]; got {tuple(n)}")
+        if cu_k is None or cu_k is cu_q:
+            cq = _dense(cu_q, "cu_q", self.dev, None, _I32)
+            return n[0] - 1, cq, cq
+        if cu_k.shape != n:
+            raise ValueError(f"cu_q {tuple(n)} and cu_k {tuple(cu_k.shape)} hold different sequence counts")
+        return n[0] - 1, _dense(cu_q, "cu_q", self.dev, None, _I32), _dense(cu_k, "cu_k", self.dev, None, _I32)
 
     def _shapes(self, q, k):
         if q.dim() != 3 or k.dim() != 3:
             raise ValueError("q, k and v must be [rows, heads, head_dim]")
         return (q.shape[0], self.heads, self.head_dim), (k.shape[0], self.kv_heads, self.head_dim)
 
-    def _workspace(self, n, nq, nk, backward):
-        nbytes = max(B.pe_attention_workspace(self.h, n, nq, nk, backward), 0)
-        return (torch.empty(nbytes, dtype=torch.uint8, device=self.dev) if nbytes else None), nbytes
+    def _workspace(self, q, n, nq, nk, backward):
+        """(tensor or None, pointer or None, bytes)"""
+        nbytes = B.pe_attention_workspace(self.h, n, nq, nk, backward)
+        if nbytes <= 0:
+            return None, None, 0
+        ws = q.new_empty(nbytes, dtype=torch.uint8)
+        return ws, ws.data_ptr(), nbytes
 
     def forward(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
                 cu_k: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, lse: bool = True,
@@ -251,19 +274,19 @@ class Attention:
         strides that are multiples of 8), cu_q and cu_k int32 [n_seq + 1] on the
         device (cu_k None: cu_q).  Returns (out [Nq, heads, D] bf16, lse [heads,
         Nq] fp32 or None).  Rows of no sequence are not written."""
-        cu_k = cu_q if cu_k is None else cu_k
+        d = self.dev
         n, cq, ck = self._cu(cu_q, cu_k)
+        if _elsewhere(d, stream):
+            with _on(d, stream):
+                return self.forward(q, k, v, cu_q, cu_k, out, lse)
         sq, sk = self._shapes(q, k)
-        d, bf = self.dev, torch.bfloat16
-        ctx, st = _on(d, stream)
-        with ctx:
-            if out is None:
-                out = torch.empty(sq, dtype=bf, device=d)
-            stat = torch.empty((self.heads, sq[0]), dtype=torch.float32, device=d) if lse else None
-            ws, nbytes = self._workspace(n, sq[0], sk[0], False)
-            B.pe_attention_forward(self.h, n, cq, sq[0], ck, sk[0], _heads(q, "q", d, bf, sq), _heads(k, "k", d, bf, sk),
-                                   _heads(v, "v", d, bf, sk), _heads(out, "out", d, bf, sq),
-                                   stat.data_ptr() if lse else None, ws.data_ptr() if nbytes else None, nbytes, st)
+        qs, ks, vs = _heads(q, "q", d, _BF16, sq), _heads(k, "k", d, _BF16, sk), _heads(v, "v", d, _BF16, sk)
+        if out is None:
+            out = q.new_empty(sq)
+        stat = q.new_empty((self.heads, sq[0]), dtype=_F32) if lse else None
+        ws, wp, nbytes = self._workspace(q, n, sq[0], sk[0], False)
+        B.pe_attention_forward(self.h, n, cq, sq[0], ck, sk[0], qs, ks, vs, _heads(out, "out", d, _BF16, sq),
+                               stat.data_ptr() if lse else None, wp, nbytes, _raw(d))
         return out, stat
 
     def backward(self, dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
@@ -272,22 +295,22 @@ class Attention:
                  dv: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
         """(dq, dk, dv) for the gradient dout of out; out and lse are forward's.
         dq, dk and dv may be given (slices of one packed gradient, for instance)."""
-        cu_k = cu_q if cu_k is None else cu_k
+        d = self.dev
         n, cq, ck = self._cu(cu_q, cu_k)
+        if _elsewhere(d, stream):
+            with _on(d, stream):
+                return self.backward(dout, q, k, v, out, lse, cu_q, cu_k, dq, dk, dv)
         sq, sk = self._shapes(q, k)
-        d, bf = self.dev, torch.bfloat16
-        lp = _dense(lse, "lse", d, (self.heads, sq[0]), torch.float32)
-        ctx, st = _on(d, stream)
-        with ctx:
-            dq = torch.empty(sq, dtype=bf, device=d) if dq is None else dq
-            dk = torch.empty(sk, dtype=bf, device=d) if dk is None else dk
-            dv = torch.empty(sk, dtype=bf, device=d) if dv is None else dv
-            ws, nbytes = self._workspace(n, sq[0], sk[0], True)
-            B.pe_attention_backward(self.h, n, cq, sq[0], ck, sk[0], _heads(q, "q", d, bf, sq), _heads(k, "k", d, bf, sk),
-                                    _heads(v, "v", d, bf, sk), _heads(out, "out", d, bf, sq), lp,
-                                    _heads(dout, "dout", d, bf, sq), _heads(dq, "dq", d, bf, sq),
-                                    _heads(dk, "dk", d, bf, sk), _heads(dv, "dv", d, bf, sk),
-                                    ws.data_ptr() if nbytes else None, nbytes, st)
+        lp = _dense(lse, "lse", d, (self.heads, sq[0]), _F32)
+        args = [_heads(t, name, d, _BF16, s) for t, name, s in
+                ((q, "q", sq), (k, "k", sk), (v, "v", sk), (out, "out", sq), (dout, "dout", sq))]
+        dq = q.new_empty(sq) if dq is None else dq
+        dk = k.new_empty(sk) if dk is None else dk
+        dv = k.new_empty(sk) if dv is None else dv
+        ws, wp, nbytes = self._workspace(q, n, sq[0], sk[0], True)
+        B.pe_attention_backward(self.h, n, cq, sq[0], ck, sk[0], args[0], args[1], args[2], args[3], lp, args[4],
+                                _heads(dq, "dq", d, _BF16, sq), _heads(dk, "dk", d, _BF16, sk),
+                                _heads(dv, "dv", d, _BF16, sk), wp, nbytes, _raw(d))
         return dq, dk, dv
 
     def last_error(self) -> int:
