@@ -113,65 +113,115 @@ struct RopeParams {
     RopeSide s[2];               // q, k
     const int32_t *pos;          // [axes, N]
     int64_t N;
-    int pairs, tail, rows;       // S, D - 2 S, rows per block
+    int pairs, tail;             // S, D - 2 S
     float sign;
     uint8_t axis[128];           // of pair i
     double turns[128];           // rate of pair i in turns: rate / (2 pi)
 };
 
+// VEC elements as one access, and as fp32.
 template <class T, int VEC>
 struct alignas(sizeof(T) * VEC) Pack {
     T v[VEC];
+    __device__ __forceinline__ void get(float (&f)[VEC]) const {
+        if constexpr (sizeof(T) == 2 && VEC > 1) {
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(v);
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) f[2 * i] = bf16lo_to_f32(w[i]), f[2 * i + 1] = bf16hi_to_f32(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) f[i] = to_f32(v[i]);
+        }
+    }
+    __device__ __forceinline__ void set(const float (&f)[VEC]) {
+        if constexpr (sizeof(T) == 2 && VEC > 1) {
+            uint32_t *w = reinterpret_cast<uint32_t *>(v);
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = from_f32<T>(f[i]);
+        }
+    }
 };
 
-// A block turns `rows` rows.  Their cosines and sines are computed once into
-// shared memory (all heads of q and k share them): the angle in turns is a
-// 64-bit product reduced to [-1/2, 1/2] exactly, so a position of a million
-// costs no accuracy, and 64 bits are spent on S values a row, not on every
-// element.  Then each thread turns VEC pairs at a time.
+constexpr int kRopeRows = 8;     // rows, and warps, of a block
+
+// A warp turns a row.  Its cosines and sines are computed once for all heads of q
+// and k: the angle in turns is a 64-bit product reduced to [-1/2, 1/2] exactly, so
+// a position of a million costs no accuracy, and 64 bits are spent on S values a
+// row, not on every element.  A lane keeps VEC of them in registers and takes the
+// same VEC pairs of one head after the other, the lanes as many heads side by side
+// as fit; two heads' loads are on their way ahead of the arithmetic, the first two
+// while the cosines are computed.
 template <class T, int VEC>
-__global__ void __launch_bounds__(256) pe_rope_kernel(const __grid_constant__ RopeParams P) {
-    extern __shared__ float2 cs[];                       // [rows][pairs] (cos, sin)
-    const int S = P.pairs;
-    const int64_t row0 = (int64_t)blockIdx.x * P.rows;
-    const int rows = (int)(P.N - row0 < P.rows ? P.N - row0 : P.rows);
-    for (int i = threadIdx.x; i < rows * S; i += blockDim.x) {
-        const int r = i / S, p = i - r * S;
-        const double t = (double)P.pos[(int64_t)P.axis[p] * P.N + row0 + r] * P.turns[p];
+__global__ void __launch_bounds__(32 * kRopeRows, sizeof(T) * VEC == 16 ? 4 : 6) pe_rope_kernel(const __grid_constant__ RopeParams P) {
+    extern __shared__ float2 all[];                      // [kRopeRows][pairs] (cos, sin)
+    using V = Pack<T, VEC>;
+    const int S = P.pairs, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = (int64_t)blockIdx.x * kRopeRows + warp;
+    if (row >= P.N) return;
+    const int sv = S / VEC, per_head = sv + P.tail / VEC, across = per_head < 32 ? per_head : 32;
+    const int step = 32 / across, h0 = lane / across, heads0 = P.s[0].heads, heads = heads0 + P.s[1].heads;
+    const T *in0 = static_cast<const T *>(P.s[0].in) + row * P.s[0].in_row;
+    const T *in1 = static_cast<const T *>(P.s[1].in) + row * P.s[1].in_row - heads0 * P.s[1].in_head;
+    T *out0 = static_cast<T *>(P.s[0].out) + row * P.s[0].out_row;
+    T *out1 = static_cast<T *>(P.s[1].out) + row * P.s[1].out_row - heads0 * P.s[1].out_head;
+    auto source = [&](int h) { return h < heads0 ? in0 + h * P.s[0].in_head : in1 + h * P.s[1].in_head; };
+    auto target = [&](int h) { return h < heads0 ? out0 + h * P.s[0].out_head : out1 + h * P.s[1].out_head; };
+    V a[2], b[2];
+    auto fetch = [&](V &x, V &y, int h, int v) {
+        if (h >= heads || h0 >= step) return;
+        const T *p = source(h) + (v < sv ? v * VEC : S + v * VEC);           // the tail begins at 2 S
+        x = *reinterpret_cast<const V *>(p);
+        if (v < sv) y = *reinterpret_cast<const V *>(p + S);
+    };
+    int v = lane - h0 * across;
+    fetch(a[0], b[0], h0, v);
+    fetch(a[1], b[1], h0 + step, v);
+    float2 *cs = all + warp * S;
+    for (int p = lane; p < S; p += 32) {
+        const double t = (double)P.pos[(int64_t)P.axis[p] * P.N + row] * P.turns[p];
         const float u = (float)(t - rint(t));
         float s, c;
         sincospif(2.0f * u, &s, &c);
-        cs[i] = make_float2(c, P.sign * s);
+        cs[p] = make_float2(c, P.sign * s);
     }
-    __syncthreads();
-    const int sv = S / VEC, tv = P.tail / VEC, per_head = sv + tv;
-    const int heads = P.s[0].heads + P.s[1].heads, per_row = heads * per_head;
-    for (int i = threadIdx.x; i < rows * per_row; i += blockDim.x) {
-        const int r = i / per_row, j = i - r * per_row;
-        int h = j / per_head;
-        const int v = j - h * per_head;
-        const bool second = h >= P.s[0].heads;
-        const RopeSide &s = P.s[second];
-        if (second) h -= P.s[0].heads;
-        const T *in = static_cast<const T *>(s.in) + (row0 + r) * s.in_row + h * s.in_head;
-        T *out = static_cast<T *>(s.out) + (row0 + r) * s.out_row + h * s.out_head;
-        using V = Pack<T, VEC>;
-        if (v < sv) {
-            const V a = *reinterpret_cast<const V *>(in + v * VEC), b = *reinterpret_cast<const V *>(in + S + v * VEC);
-            V x, y;
+    __syncwarp();
+    if (h0 >= step) return;
+    for (; v < per_head; v += across) {
+        const bool turn = v < sv;
+        float2 t[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float2 t = cs[r * S + v * VEC + e];
-                const float f = to_f32(a.v[e]), g = to_f32(b.v[e]);
-                // the roundings are written out, so that every VEC gives the same bits
-                x.v[e] = from_f32<T>(__fmaf_rn(f, t.x, -__fmul_rn(g, t.y)));
-                y.v[e] = from_f32<T>(__fmaf_rn(g, t.x, __fmul_rn(f, t.y)));
+        for (int e = 0; e < VEC; ++e) t[e] = turn ? cs[v * VEC + e] : make_float2(1.f, 0.f);
+        for (int h = h0; h < heads; h += 2 * step) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (h + u * step >= heads) break;
+                T *o = target(h + u * step) + (turn ? v * VEC : S + v * VEC);
+                V x = a[u], y;
+                if (turn) {
+                    float f[VEC], g[VEC];
+                    a[u].get(f);
+                    b[u].get(g);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        // the roundings are written out, so that every VEC gives the same bits
+                        const float p = __fmaf_rn(f[e], t[e].x, -__fmul_rn(g[e], t[e].y));
+                        g[e] = __fmaf_rn(g[e], t[e].x, __fmul_rn(f[e], t[e].y));
+                        f[e] = p;
+                    }
+                    x.set(f);
+                    y.set(g);
+                    *reinterpret_cast<V *>(o + S) = y;
+                }
+                *reinterpret_cast<V *>(o) = x;
+                fetch(a[u], b[u], h + (2 + u) * step, v);
             }
-            *reinterpret_cast<V *>(out + v * VEC) = x;
-            *reinterpret_cast<V *>(out + S + v * VEC) = y;
-        } else if (in != out) {
-            const int e = 2 * S + (v - sv) * VEC;
-            *reinterpret_cast<V *>(out + e) = *reinterpret_cast<const V *>(in + e);
+        }
+        if (v + across < per_head) {
+            fetch(a[0], b[0], h0, v + across);
+            fetch(a[1], b[1], h0 + step, v + across);
         }
     }
 }
@@ -179,9 +229,9 @@ __global__ void __launch_bounds__(256) pe_rope_kernel(const __grid_constant__ Ro
 // ------------------------------------------------------------- layer norm
 //
 // TPR threads hold one row in registers, VPT groups of 8 elements each, so x is
-// read once and the variance is taken from the deviations.  A warp per row up
-// to 1280 features, 128 threads up to 4096, 512 beyond (VPT <= 5 keeps the
-// backward kernel's 16 sums per group in registers).
+// read once and the variance is taken from the deviations.  The backward kernel
+// keeps 16 sums per group beside the row, and the next row on its way: VPT is at
+// most 5 (bf16) or 3 (fp32) for that, and rows take as many threads as it needs.
 
 // Sum of v over the TPR threads of a row (all of them get it); blocks hold
 // blockDim / TPR rows.  `red`: TPR / 32 floats per row.
@@ -201,6 +251,27 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
     return v;
 }
 
+// 8 elements as they are stored (loaded past L1: each row is read once), and as fp32.
+template <class T> struct Raw;
+template <> struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = __ldcg(reinterpret_cast<const float4 *>(p)), b = __ldcg(reinterpret_cast<const float4 *>(p + 4));
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+};
+template <> struct Raw<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = __ldcg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[2 * i] = bf16lo_to_f32(w[i]), v[2 * i + 1] = bf16hi_to_f32(w[i]);
+    }
+};
+
 struct NormParams {
     const void *x, *dy, *gamma, *beta;
     void *y;                      // forward: y; backward: dx
@@ -212,7 +283,7 @@ struct NormParams {
 };
 
 template <int TPR>
-constexpr int kNormThreads = TPR == 512 ? 512 : 128;
+constexpr int kNormThreads = TPR > 128 ? TPR : 128;
 
 template <class T, int TPR, int VPT>
 __global__ void __launch_bounds__(kNormThreads<TPR>) pe_norm_fwd_kernel(const NormParams P) {
@@ -220,13 +291,14 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) pe_norm_fwd_kernel(const No
     constexpr int kRows = kNormThreads<TPR> / TPR;
     const int t = threadIdx.x % TPR, nv = P.E / 8;
     const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
-    if (TPR == 32 && row >= P.N) return;                  // wider rows: one per block
+    const bool live = row < P.N;                          // rows of several warps meet at barriers
+    if (TPR == 32 && !live) return;
     const T *x = static_cast<const T *>(P.x) + row * P.E;
     float v[VPT][8];
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        if (t + i * TPR < nv) {
+        if (live && t + i * TPR < nv) {
             load8(x + 8 * (t + i * TPR), v[i]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s += v[i][e];
@@ -236,14 +308,14 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) pe_norm_fwd_kernel(const No
     float q = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
-        if (t + i * TPR < nv)
+        if (live && t + i * TPR < nv)
 #pragma unroll
             for (int e = 0; e < 8; ++e) q += (v[i][e] - mean) * (v[i][e] - mean);
     const float rstd = 1.0f / sqrtf(row_sum<TPR>(q, red) / (float)P.E + P.eps);
     T *y = static_cast<T *>(P.y) + row * P.E;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        if (t + i * TPR < nv) {
+        if (live && t + i * TPR < nv) {
             const int e0 = 8 * (t + i * TPR);
             float g[8], b[8];
             load8_weight(P.gamma, P.w_f32, e0, 1.f, g);
@@ -253,7 +325,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) pe_norm_fwd_kernel(const No
             store8(y + e0, v[i]);
         }
     }
-    if (P.mean && t == 0) {
+    if (P.mean && live && t == 0) {
         P.mean[row] = mean;
         P.rstd[row] = rstd;
     }
@@ -262,12 +334,14 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) pe_norm_fwd_kernel(const No
 // Each block takes rows blockIdx, blockIdx + gridDim, ... (in groups of its rows
 // at once), writes dx, and keeps the sums over its rows of dy * xh and dy for
 // its features in registers; they go to part[blockIdx] once.  No atomics: the
-// order of every sum is fixed by the sizes.
+// order of every sum is fixed by the sizes.  The next row's loads are in flight
+// while a row is worked on (not with 1024 threads, whose registers are full).
 template <class T, int TPR, int VPT>
 __global__ void __launch_bounds__(kNormThreads<TPR>) pe_norm_bwd_kernel(const NormParams P) {
     extern __shared__ float sums[];                       // [rows per block - 1][2][E] when part
     __shared__ float red[kNormThreads<TPR> / 32];
     constexpr int kRows = kNormThreads<TPR> / TPR;
+    constexpr bool kAhead = TPR < 1024;
     const int t = threadIdx.x % TPR, lane_row = threadIdx.x / TPR, nv = P.E / 8;
     const float inv_e = 1.0f / (float)P.E;
     float dg[VPT][8], db[VPT][8];
@@ -275,42 +349,75 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) pe_norm_bwd_kernel(const No
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) dg[i][e] = db[i][e] = 0.f;
-    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < P.N; r0 += (int64_t)gridDim.x * kRows) {
+    // gamma stays in registers: every row passing through L1 would push it out of there
+    float gm[kAhead ? VPT : 1][8];
+    if (kAhead) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (t + i * TPR < nv) load8_weight(P.gamma, P.w_f32, 8 * (t + i * TPR), 1.f, gm[i]);
+    }
+    Raw<T> xr[VPT], yr[VPT], xn[kAhead ? VPT : 1], yn[kAhead ? VPT : 1];
+    float mean = 0.f, rstd = 0.f, mean_n = 0.f, rstd_n = 0.f;
+    auto load = [&](int64_t row, Raw<T> *x, Raw<T> *y, float &m, float &r) {
+        if (row >= P.N) return;
+        const T *px = static_cast<const T *>(P.x) + row * P.E, *py = static_cast<const T *>(P.dy) + row * P.E;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (t + i * TPR < nv) {
+                x[i].load(px + 8 * (t + i * TPR));
+                y[i].load(py + 8 * (t + i * TPR));
+            }
+        m = P.mean[row];
+        r = P.rstd[row];
+    };
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    if (kAhead) load((int64_t)blockIdx.x * kRows + lane_row, xr, yr, mean, rstd);
+    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < P.N; r0 += step) {
         const int64_t row = r0 + lane_row;
-        if (TPR == 32 && row >= P.N) break;               // whole warps; wider rows: one per block
-        const T *x = static_cast<const T *>(P.x) + row * P.E, *dy = static_cast<const T *>(P.dy) + row * P.E;
-        const float mean = P.mean[row], rstd = P.rstd[row];
-        float xh[VPT][8], a[VPT][8];
-        float s1 = 0.f, s2 = 0.f;
+        const bool live = row < P.N;
+        if (kAhead) load(row + step, xn, yn, mean_n, rstd_n);
+        else load(row, xr, yr, mean, rstd);
+        float p1[2] = {0.f, 0.f}, p2[2] = {0.f, 0.f};        // two chains of additions each
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            if (t + i * TPR < nv) {
-                const int e0 = 8 * (t + i * TPR);
-                load8(x + e0, xh[i]);
-                load8(dy + e0, a[i]);
-                float g[8];
-                load8_weight(P.gamma, P.w_f32, e0, 1.f, g);
+            if (live && t + i * TPR < nv) {
+                float x[8], a[8];
+                xr[i].get(x);
+                yr[i].get(a);
+                float (&g)[8] = gm[kAhead ? i : 0];
+                if (!kAhead) load8_weight(P.gamma, P.w_f32, 8 * (t + i * TPR), 1.f, g);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    xh[i][e] = (xh[i][e] - mean) * rstd;
-                    dg[i][e] += a[i][e] * xh[i][e];
-                    db[i][e] += a[i][e];
-                    a[i][e] *= g[e];
-                    s1 += a[i][e];
-                    s2 += a[i][e] * xh[i][e];
+                    const float xh = (x[e] - mean) * rstd;
+                    dg[i][e] += a[e] * xh;
+                    db[i][e] += a[e];
+                    a[e] *= g[e];
+                    p1[e & 1] += a[e];
+                    p2[e & 1] += a[e] * xh;
                 }
             }
         }
-        s1 = row_sum<TPR>(s1, red) * inv_e;
-        s2 = row_sum<TPR>(s2, red) * inv_e;
+        const float s1 = row_sum<TPR>(p1[0] + p1[1], red) * inv_e;
+        const float s2 = row_sum<TPR>(p2[0] + p2[1], red) * inv_e;
         T *dx = static_cast<T *>(P.y) + row * P.E;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            if (t + i * TPR < nv) {
+            if (live && t + i * TPR < nv) {
+                float x[8], a[8];
+                xr[i].get(x);
+                yr[i].get(a);
+                float (&g)[8] = gm[kAhead ? i : 0];
+                if (!kAhead) load8_weight(P.gamma, P.w_f32, 8 * (t + i * TPR), 1.f, g);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) a[i][e] = rstd * (a[i][e] - s1 - xh[i][e] * s2);
-                store8(dx + 8 * (t + i * TPR), a[i]);
+                for (int e = 0; e < 8; ++e) a[e] = rstd * (a[e] * g[e] - s1 - (x[e] - mean) * rstd * s2);
+                store8(dx + 8 * (t + i * TPR), a);
             }
+        }
+        if (kAhead) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) xr[i] = xn[i], yr[i] = yn[i];
+            mean = mean_n;
+            rstd = rstd_n;
         }
     }
     if (!P.part) return;
@@ -344,22 +451,25 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) pe_norm_bwd_kernel(const No
     }
 }
 
-// dgamma and dbeta from `n` partial rows of 2 E: a block sums 32 columns, its 8
-// warps every 8th row, then the 8 sums in order.
-__global__ void __launch_bounds__(256) pe_norm_sum_kernel(const float *part, int n, int E, int w_f32, void *dgamma,
-                                                          void *dbeta) {
-    __shared__ float s[8][33];
+// dgamma and dbeta from `n` partial rows of 2 E: a block sums 32 columns, its 32
+// warps every 32nd row each (four loads in flight), then the 32 sums in order.
+__global__ void __launch_bounds__(1024) pe_norm_sum_kernel(const float *part, int n, int E, int w_f32, void *dgamma,
+                                                           void *dbeta) {
+    __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
-    float a = 0.f;
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
     if (col < 2 * E)
-        for (int r = w; r < n; r += 8) a += part[(int64_t)r * 2 * E + col];
-    s[w][lane] = a;
+        for (int r = w; r < n; r += 128)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (r + 32 * u < n) a[u] += part[(int64_t)(r + 32 * u) * 2 * E + col];
+    s[w][lane] = (a[0] + a[1]) + (a[2] + a[3]);
     __syncthreads();
     if (w != 0 || col >= 2 * E) return;
     float v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v += s[i][lane];
+    for (int i = 0; i < 32; ++i) v += s[i][lane];
     void *dst = col < E ? dgamma : dbeta;
     const int e = col < E ? col : col - E;
     if (w_f32) static_cast<float *>(dst)[e] = v;

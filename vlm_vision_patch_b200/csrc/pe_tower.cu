@@ -65,58 +65,66 @@ int rope_vec(const RopeParams &P, size_t es) {
 
 template <class T, int VEC>
 cudaError_t launch_rope(const RopeParams &P, cudaStream_t st) {
-    const int64_t blocks = (P.N + P.rows - 1) / P.rows;
-    pe_rope_kernel<T, VEC><<<(unsigned)blocks, 256, (size_t)P.rows * P.pairs * sizeof(float2), st>>>(P);
+    const int64_t blocks = (P.N + kRopeRows - 1) / kRopeRows;
+    pe_rope_kernel<T, VEC><<<(unsigned)blocks, 32 * kRopeRows, (size_t)kRopeRows * P.pairs * sizeof(float2), st>>>(P);
     return cudaGetLastError();
 }
 
 // ------------------------------------------------------------- layer norm
 
-// Threads per row (see pe_rows.cuh).
-int norm_tpr(int E) { return E <= 1280 ? 32 : (E <= 4096 ? 128 : 512); }
-
-// Blocks of the backward kernel: each writes one partial row of 2 E sums, so
-// there are no more than fill the GPU.
-int norm_bwd_blocks(int64_t N, int E, int sms) {
-    const int tpr = norm_tpr(E), rows = tpr == 32 ? 4 : 1;
-    return (int)std::min<int64_t>((N + rows - 1) / rows, (int64_t)sms * (tpr == 512 ? 1 : 3));
+// Threads per row (see pe_rows.cuh).  Forward: a warp up to 1280 features, then 128
+// and 256 (fewer, fuller threads beat 1024 here: 8192 fp32 features ran at 2.5 TB/s
+// with those).  Backward: as few as its sums beside two rows leave registers for.
+int norm_tpr(int E, bool f32, bool backward) {
+    if (!backward) return E <= 1280 ? 32 : (E <= 4096 ? 128 : 256);
+    if (E <= (f32 ? 768 : 1280)) return 32;
+    if (f32 && E <= 1536) return 64;
+    return E <= (f32 ? 3072 : 4096) ? 128 : 1024;
 }
 
-template <class T, int TPR, int VPT>
-cudaError_t launch_norm(const NormParams &P, bool backward, int blocks, cudaStream_t st) {
-    constexpr int kThreads = kNormThreads<TPR>;
-    if (!backward) {
-        pe_norm_fwd_kernel<T, TPR, VPT><<<(unsigned)blocks, kThreads, 0, st>>>(P);
+int norm_rows(int tpr) { return tpr > 128 ? 1 : 128 / tpr; }          // rows per block
+
+// Blocks of the backward kernel: as many as are resident, since each writes one
+// partial row of 2 E sums.
+int norm_bwd_blocks(int64_t N, int E, bool f32, int sms) {
+    const int tpr = norm_tpr(E, f32, true), rows = norm_rows(tpr);
+    return (int)std::min<int64_t>((N + rows - 1) / rows, (int64_t)sms * (tpr == 1024 ? 1 : 2));
+}
+
+template <class T, bool BACKWARD, int TPR, int VPT>
+cudaError_t launch_norm(const NormParams &P, int blocks, cudaStream_t st) {
+    if constexpr (!BACKWARD) {
+        pe_norm_fwd_kernel<T, TPR, VPT><<<(unsigned)blocks, kNormThreads<TPR>, 0, st>>>(P);
     } else {
-        const size_t smem = P.part ? (size_t)(kThreads / TPR - 1) * 2 * P.E * sizeof(float) : 0;
-        pe_norm_bwd_kernel<T, TPR, VPT><<<(unsigned)blocks, kThreads, smem, st>>>(P);
+        const size_t smem = P.part ? (size_t)(kNormThreads<TPR> / TPR - 1) * 2 * P.E * sizeof(float) : 0;
+        pe_norm_bwd_kernel<T, TPR, VPT><<<(unsigned)blocks, kNormThreads<TPR>, smem, st>>>(P);
     }
     return cudaGetLastError();
 }
 
-template <class T>
-cudaError_t dispatch_norm(const NormParams &P, bool backward, int blocks, cudaStream_t st) {
-    const int tpr = norm_tpr(P.E), vpt = (P.E / 8 + tpr - 1) / tpr;
-    if (tpr == 32) {
-        switch (vpt) {
-            case 1: return launch_norm<T, 32, 1>(P, backward, blocks, st);
-            case 2: return launch_norm<T, 32, 2>(P, backward, blocks, st);
-            case 3: return launch_norm<T, 32, 3>(P, backward, blocks, st);
-            case 4: return launch_norm<T, 32, 4>(P, backward, blocks, st);
-            default: return launch_norm<T, 32, 5>(P, backward, blocks, st);
-        }
+// The kernel of VPT = lo .. hi groups per thread.
+template <class T, bool BACKWARD, int TPR, int LO, int HI>
+cudaError_t pick_norm(const NormParams &P, int vpt, int blocks, cudaStream_t st) {
+    if constexpr (LO < HI) {
+        if (vpt > LO) return pick_norm<T, BACKWARD, TPR, LO + 1, HI>(P, vpt, blocks, st);
     }
-    if (tpr == 128) {
-        switch (vpt) {
-            case 2: return launch_norm<T, 128, 2>(P, backward, blocks, st);
-            case 3: return launch_norm<T, 128, 3>(P, backward, blocks, st);
-            default: return launch_norm<T, 128, 4>(P, backward, blocks, st);
-        }
-    }
-    switch (vpt) {
-        case 2: return launch_norm<T, 512, 2>(P, backward, blocks, st);
-        case 3: return launch_norm<T, 512, 3>(P, backward, blocks, st);
-        default: return launch_norm<T, 512, 4>(P, backward, blocks, st);
+    return launch_norm<T, BACKWARD, TPR, LO>(P, blocks, st);
+}
+
+template <class T, bool BACKWARD>
+cudaError_t dispatch_norm(const NormParams &P, int blocks, cudaStream_t st) {
+    constexpr bool kF32 = sizeof(T) == 4;
+    const int tpr = norm_tpr(P.E, kF32, BACKWARD), vpt = (P.E / 8 + tpr - 1) / tpr;
+    if constexpr (!BACKWARD) {
+        if (tpr == 32) return pick_norm<T, false, 32, 1, 5>(P, vpt, blocks, st);
+        if (tpr == 128) return pick_norm<T, false, 128, 2, 4>(P, vpt, blocks, st);
+        return pick_norm<T, false, 256, 3, 8>(P, vpt, blocks, st);
+    } else {
+        if (tpr == 32) return pick_norm<T, true, 32, 1, kF32 ? 3 : 5>(P, vpt, blocks, st);
+        if constexpr (kF32)
+            if (tpr == 64) return pick_norm<T, true, 64, 2, 3>(P, vpt, blocks, st);
+        if (tpr == 128) return pick_norm<T, true, 128, 2, kF32 ? 3 : 4>(P, vpt, blocks, st);
+        return pick_norm<T, true, 1024, 1, 2>(P, vpt, blocks, st);
     }
 }
 
@@ -305,7 +313,6 @@ pe_status pe_rope(pe_heads q, pe_heads k, pe_dtype dt, int64_t N, int Hq, int Hk
             P.axis[i] = (uint8_t)a;
             P.turns[i] = std::pow(theta, axial ? -(double)j / sections[a] : -(double)i / (double)S) / two_pi;
         }
-    P.rows = 8;
     cudaStream_t st = (cudaStream_t)stream;
     const int vec = rope_vec(P, es);
     if (dt == PE_F32) {
@@ -340,15 +347,17 @@ pe_status pe_layernorm_forward(const void *x, pe_dtype dt, int64_t N, int E, con
     P.E = E;
     P.w_f32 = w_dt == PE_F32;
     P.eps = eps;
-    const int rows = norm_tpr(E) == 32 ? 4 : 1, blocks = (int)((N + rows - 1) / rows);
+    const int rows = norm_rows(norm_tpr(E, dt == PE_F32, false)), blocks = (int)((N + rows - 1) / rows);
     cudaStream_t st = (cudaStream_t)stream;
-    return finish(dt == PE_F32 ? dispatch_norm<float>(P, false, blocks, st)
-                               : dispatch_norm<__nv_bfloat16>(P, false, blocks, st));
+    return finish(dt == PE_F32 ? dispatch_norm<float, false>(P, blocks, st)
+                               : dispatch_norm<__nv_bfloat16, false>(P, blocks, st));
 }
 
 int64_t pe_layernorm_backward_workspace(int64_t N, int E) {
     if (check_norm(PE_F32, PE_F32, N, E) != PE_OK) return -1;
-    return (int64_t)std::max(norm_bwd_blocks(N, E, current_sms()), 0) * 2 * E * (int64_t)sizeof(float);
+    const int sms = current_sms();
+    return (int64_t)std::max(norm_bwd_blocks(N, E, false, sms), norm_bwd_blocks(N, E, true, sms)) * 2 * E *
+           (int64_t)sizeof(float);
 }
 
 pe_status pe_layernorm_backward(const void *dy, const void *x, pe_dtype dt, int64_t N, int E, const void *gamma,
@@ -363,7 +372,7 @@ pe_status pe_layernorm_backward(const void *dy, const void *x, pe_dtype dt, int6
     if (!aligned_to(mean, 4) || !aligned_to(rstd, 4)) return PE_ERR_ALIGN;
     const int sms = current_sms();
     if (sms < 1) return PE_ERR_CUDA;
-    const int blocks = norm_bwd_blocks(N, E, sms);
+    const int blocks = norm_bwd_blocks(N, E, dt == PE_F32, sms);
     if (dgamma && N > 0) {
         if (!ws) return PE_ERR_INVALID_ARG;
         if (ws_bytes < (int64_t)blocks * 2 * E * (int64_t)sizeof(float)) return PE_ERR_SHAPE;
@@ -382,12 +391,12 @@ pe_status pe_layernorm_backward(const void *dy, const void *x, pe_dtype dt, int6
     P.w_f32 = w_dt == PE_F32;
     cudaStream_t st = (cudaStream_t)stream;
     if (N > 0) {
-        const cudaError_t e = dt == PE_F32 ? dispatch_norm<float>(P, true, blocks, st)
-                                           : dispatch_norm<__nv_bfloat16>(P, true, blocks, st);
+        const cudaError_t e = dt == PE_F32 ? dispatch_norm<float, true>(P, blocks, st)
+                                           : dispatch_norm<__nv_bfloat16, true>(P, blocks, st);
         if (e != cudaSuccess) return PE_ERR_CUDA;
     }
     if (!dgamma) return PE_OK;
-    pe_norm_sum_kernel<<<(2 * E + 31) / 32, 256, 0, st>>>(P.part, blocks, E, P.w_f32, dgamma, dbeta);
+    pe_norm_sum_kernel<<<(2 * E + 31) / 32, 1024, 0, st>>>(P.part, blocks, E, P.w_f32, dgamma, dbeta);
     return finish(cudaGetLastError());
 }
 
