@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 
 #include "pe_device.cuh"
+#include "pe_packed.cuh"
 
 namespace pe {
 
@@ -258,17 +259,18 @@ template <> struct Raw<float> {
     __device__ __forceinline__ void load(const float *p) {
         a = __ldcg(reinterpret_cast<const float4 *>(p)), b = __ldcg(reinterpret_cast<const float4 *>(p + 4));
     }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    __device__ __forceinline__ void get(float2 (&v)[4]) const {
+        v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w);
+        v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
     }
 };
 template <> struct Raw<__nv_bfloat16> {
     uint4 a;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = __ldcg(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
+    __device__ __forceinline__ void get(float2 (&v)[4]) const {
         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[2 * i] = bf16lo_to_f32(w[i]), v[2 * i + 1] = bf16hi_to_f32(w[i]);
+        for (int i = 0; i < 4; ++i) v[i] = make_float2(bf16lo_to_f32(w[i]), bf16hi_to_f32(w[i]));
     }
 };
 
@@ -344,17 +346,23 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) pe_norm_bwd_kernel(const No
     constexpr bool kAhead = TPR < 1024;
     const int t = threadIdx.x % TPR, lane_row = threadIdx.x / TPR, nv = P.E / 8;
     const float inv_e = 1.0f / (float)P.E;
-    float dg[VPT][8], db[VPT][8];
+    float2 dg[VPT][4], db[VPT][4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dg[i][e] = db[i][e] = 0.f;
+        for (int e = 0; e < 4; ++e) dg[i][e] = db[i][e] = both(0.f);
     // gamma stays in registers: every row passing through L1 would push it out of there
-    float gm[kAhead ? VPT : 1][8];
+    float2 gm[kAhead ? VPT : 1][4];
+    auto load_gamma = [&](int i, float2 (&g)[4]) {
+        float v[8];
+        load8_weight(P.gamma, P.w_f32, 8 * (t + i * TPR), 1.f, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[e] = make_float2(v[2 * e], v[2 * e + 1]);
+    };
     if (kAhead) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            if (t + i * TPR < nv) load8_weight(P.gamma, P.w_f32, 8 * (t + i * TPR), 1.f, gm[i]);
+            if (t + i * TPR < nv) load_gamma(i, gm[i]);
     }
     Raw<T> xr[VPT], yr[VPT], xn[kAhead ? VPT : 1], yn[kAhead ? VPT : 1];
     float mean = 0.f, rstd = 0.f, mean_n = 0.f, rstd_n = 0.f;
@@ -377,40 +385,46 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) pe_norm_bwd_kernel(const No
         const bool live = row < P.N;
         if (kAhead) load(row + step, xn, yn, mean_n, rstd_n);
         else load(row, xr, yr, mean, rstd);
-        float p1[2] = {0.f, 0.f}, p2[2] = {0.f, 0.f};        // two chains of additions each
+        const float2 off = both(-mean), scale = both(rstd);
+        float2 p1 = both(0.f), p2 = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (live && t + i * TPR < nv) {
-                float x[8], a[8];
+                float2 x[4], a[4];
                 xr[i].get(x);
                 yr[i].get(a);
-                float (&g)[8] = gm[kAhead ? i : 0];
-                if (!kAhead) load8_weight(P.gamma, P.w_f32, 8 * (t + i * TPR), 1.f, g);
+                float2 (&g)[4] = gm[kAhead ? i : 0];
+                if (!kAhead) load_gamma(i, g);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float xh = (x[e] - mean) * rstd;
-                    dg[i][e] += a[e] * xh;
-                    db[i][e] += a[e];
-                    a[e] *= g[e];
-                    p1[e & 1] += a[e];
-                    p2[e & 1] += a[e] * xh;
+                for (int e = 0; e < 4; ++e) {
+                    const float2 xh = mul2(add2(x[e], off), scale);
+                    dg[i][e] = fma2(a[e], xh, dg[i][e]);
+                    db[i][e] = add2(db[i][e], a[e]);
+                    a[e] = mul2(a[e], g[e]);
+                    p1 = add2(p1, a[e]);
+                    p2 = fma2(a[e], xh, p2);
                 }
             }
         }
-        const float s1 = row_sum<TPR>(p1[0] + p1[1], red) * inv_e;
-        const float s2 = row_sum<TPR>(p2[0] + p2[1], red) * inv_e;
+        const float s1 = row_sum<TPR>(p1.x + p1.y, red) * inv_e;
+        const float s2 = row_sum<TPR>(p2.x + p2.y, red) * inv_e;
         T *dx = static_cast<T *>(P.y) + row * P.E;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (live && t + i * TPR < nv) {
-                float x[8], a[8];
+                float2 x[4], a[4];
                 xr[i].get(x);
                 yr[i].get(a);
-                float (&g)[8] = gm[kAhead ? i : 0];
-                if (!kAhead) load8_weight(P.gamma, P.w_f32, 8 * (t + i * TPR), 1.f, g);
+                float2 (&g)[4] = gm[kAhead ? i : 0];
+                if (!kAhead) load_gamma(i, g);
+                float o[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) a[e] = rstd * (a[e] * g[e] - s1 - (x[e] - mean) * rstd * s2);
-                store8(dx + 8 * (t + i * TPR), a);
+                for (int e = 0; e < 4; ++e) {
+                    const float2 xh = mul2(add2(x[e], off), scale);
+                    const float2 r = mul2(scale, fma2(xh, both(-s2), fma2(a[e], g[e], both(-s1))));
+                    o[2 * e] = r.x, o[2 * e + 1] = r.y;
+                }
+                store8(dx + 8 * (t + i * TPR), o);
             }
         }
         if (kAhead) {
@@ -422,13 +436,17 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) pe_norm_bwd_kernel(const No
     }
     if (!P.part) return;
     float *out = P.part + (int64_t)blockIdx.x * 2 * P.E;
+    auto put = [&](float *dst, const float2 (&v)[4]) {
+        *reinterpret_cast<float4 *>(dst) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+        *reinterpret_cast<float4 *>(dst + 4) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+    };
     if constexpr (kRows > 1) {                            // the block's rows, added in order by the first
         if (lane_row > 0) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
                 if (t + i * TPR < nv) {
-                    store8(sums + (lane_row - 1) * 2 * P.E + 8 * (t + i * TPR), dg[i]);
-                    store8(sums + (lane_row - 1) * 2 * P.E + P.E + 8 * (t + i * TPR), db[i]);
+                    put(sums + (lane_row - 1) * 2 * P.E + 8 * (t + i * TPR), dg[i]);
+                    put(sums + (lane_row - 1) * 2 * P.E + P.E + 8 * (t + i * TPR), db[i]);
                 }
         }
         __syncthreads();
@@ -439,14 +457,13 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) pe_norm_bwd_kernel(const No
         if (t + i * TPR < nv) {
             const int e0 = 8 * (t + i * TPR);
             for (int r = 0; r < kRows - 1; ++r) {
-                float u[8], w[8];
-                load8(sums + r * 2 * P.E + e0, u);
-                load8(sums + r * 2 * P.E + P.E + e0, w);
+                const float2 *u = reinterpret_cast<const float2 *>(sums + r * 2 * P.E + e0);
+                const float2 *w = reinterpret_cast<const float2 *>(sums + r * 2 * P.E + P.E + e0);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dg[i][e] += u[e], db[i][e] += w[e];
+                for (int e = 0; e < 4; ++e) dg[i][e] = add2(dg[i][e], u[e]), db[i][e] = add2(db[i][e], w[e]);
             }
-            store8(out + e0, dg[i]);
-            store8(out + P.E + e0, db[i]);
+            put(out + e0, dg[i]);
+            put(out + P.E + e0, db[i]);
         }
     }
 }
