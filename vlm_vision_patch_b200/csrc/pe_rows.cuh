@@ -229,10 +229,11 @@ __global__ void __launch_bounds__(32 * kRopeRows, sizeof(T) * VEC == 16 ? 4 : 6)
 
 // ------------------------------------------------------------- layer norm
 //
-// TPR threads hold one row in registers, VPT groups of 8 elements each, so x is
-// read once and the variance is taken from the deviations.  The backward kernel
-// keeps 16 sums per group beside the row, and the next row on its way: VPT is at
-// most 5 (bf16) or 3 (fp32) for that, and rows take as many threads as it needs.
+// TPR threads share one row.  Forward, VPT groups of 8 elements per thread stay in
+// registers: x is read once and the variance is taken from the deviations.
+// Backward, the sums of the weight's gradients stay in registers, so the rows pass
+// through shared memory: each thread copies its own 16-byte chunks there, rows
+// ahead of the one it works on, and reads only what it copied itself (no barrier).
 
 // Sum of v over the TPR threads of a row (all of them get it); blocks hold
 // blockDim / TPR rows.  `red`: TPR / 32 floats per row.
@@ -252,27 +253,42 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
     return v;
 }
 
-// 8 elements as they are stored (loaded past L1: each row is read once), and as fp32.
-template <class T> struct Raw;
-template <> struct Raw<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float *p) {
-        a = __ldcg(reinterpret_cast<const float4 *>(p)), b = __ldcg(reinterpret_cast<const float4 *>(p + 4));
-    }
-    __device__ __forceinline__ void get(float2 (&v)[4]) const {
-        v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w);
-        v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
-    }
-};
-template <> struct Raw<__nv_bfloat16> {
-    uint4 a;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = __ldcg(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void get(float2 (&v)[4]) const {
+// 16 bytes from global to shared memory, past L1 and without waiting.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most N of this thread's groups of copies are on their way.
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A chunk of 16 bytes as fp32 pairs: 8 bf16 or 4 fp32.
+template <class T>
+constexpr int kPairs = 8 / (int)sizeof(T);
+
+template <class T>
+__device__ __forceinline__ void take_chunk(const uint8_t *p, float2 (&v)[kPairs<T>]) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(p);
+    if constexpr (sizeof(T) == 4) {
+        v[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+        v[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+    } else {
         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = make_float2(bf16lo_to_f32(w[i]), bf16hi_to_f32(w[i]));
     }
-};
+}
+template <class T>
+__device__ __forceinline__ void put_chunk(T *p, const float2 (&v)[kPairs<T>]) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    } else {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                                   pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+    }
+}
 
 struct NormParams {
     const void *x, *dy, *gamma, *beta;
@@ -333,74 +349,88 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) pe_norm_fwd_kernel(const No
     }
 }
 
+template <int TPR, int CPT>
+struct NormBwd {
+    static constexpr int kThreads = kNormThreads<TPR>, kRows = kThreads / TPR;
+    static constexpr int kTensor = CPT * kThreads * 16;                   // bytes of one tensor's rows
+    static constexpr int kStages = 3 * 2 * kTensor <= 200 * 1024 ? 3 : 1; // rows on their way
+    static constexpr int kSmem = kStages * 2 * kTensor;
+    static constexpr int kResident = TPR <= 128 ? 3 : (TPR == 256 && CPT <= 4 ? 2 : 1);   // blocks of a SM
+    static_assert(kResident * (kSmem + 1280) <= 228 * 1024, "shared memory");
+};
+
 // Each block takes rows blockIdx, blockIdx + gridDim, ... (in groups of its rows
 // at once), writes dx, and keeps the sums over its rows of dy * xh and dy for
 // its features in registers; they go to part[blockIdx] once.  No atomics: the
-// order of every sum is fixed by the sizes.  The next row's loads are in flight
-// while a row is worked on (not with 1024 threads, whose registers are full).
-template <class T, int TPR, int VPT>
-__global__ void __launch_bounds__(kNormThreads<TPR>) pe_norm_bwd_kernel(const NormParams P) {
-    extern __shared__ float sums[];                       // [rows per block - 1][2][E] when part
-    __shared__ float red[kNormThreads<TPR> / 32];
-    constexpr int kRows = kNormThreads<TPR> / TPR;
-    constexpr bool kAhead = TPR < 1024;
-    const int t = threadIdx.x % TPR, lane_row = threadIdx.x / TPR, nv = P.E / 8;
+// order of every sum is fixed by the sizes.
+template <class T, int TPR, int CPT>
+__global__ void __launch_bounds__(NormBwd<TPR, CPT>::kThreads, NormBwd<TPR, CPT>::kResident)
+pe_norm_bwd_kernel(const NormParams P) {
+    using S = NormBwd<TPR, CPT>;
+    constexpr int kRows = S::kRows, kStep = S::kThreads * 16, kP = kPairs<T>;
+    extern __shared__ __align__(16) uint8_t ring[];       // [stage][x, dy][chunk][thread] of 16 bytes
+    __shared__ float red[S::kThreads / 32];
+    const int t = threadIdx.x % TPR, lane_row = threadIdx.x / TPR, chunks = P.E / (2 * kP);
     const float inv_e = 1.0f / (float)P.E;
-    float2 dg[VPT][4], db[VPT][4];
+    float2 dg[CPT][kP], db[CPT][kP], gm[CPT][kP];
+    // gamma stays in registers: every row passing by would push it out of L1
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
+    for (int i = 0; i < CPT; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dg[i][e] = db[i][e] = both(0.f);
-    // gamma stays in registers: every row passing through L1 would push it out of there
-    float2 gm[kAhead ? VPT : 1][4];
-    auto load_gamma = [&](int i, float2 (&g)[4]) {
-        float v[8];
-        load8_weight(P.gamma, P.w_f32, 8 * (t + i * TPR), 1.f, v);
+        for (int e = 0; e < kP; ++e) {
+            dg[i][e] = db[i][e] = both(0.f);
+            const int64_t at = 2 * (kP * (int64_t)(t + i * TPR) + e);
+            gm[i][e] = both(1.f);
+            if (P.gamma && t + i * TPR < chunks)
+                gm[i][e] = P.w_f32 ? *reinterpret_cast<const float2 *>(static_cast<const float *>(P.gamma) + at)
+                                   : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(
+                                         static_cast<const __nv_bfloat16 *>(P.gamma) + at));
+        }
+    uint8_t *mine = ring + threadIdx.x * 16;
+    const uint32_t mine_s = smem_addr(mine);
+    auto fetch = [&](int64_t row, int stage) {
+        if (row < P.N) {
+            const T *px = static_cast<const T *>(P.x) + row * P.E, *py = static_cast<const T *>(P.dy) + row * P.E;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) g[e] = make_float2(v[2 * e], v[2 * e + 1]);
+            for (int i = 0; i < CPT; ++i)
+                if (t + i * TPR < chunks) {
+                    const uint32_t dst = mine_s + stage * 2 * S::kTensor + i * kStep;
+                    copy16(dst, px + 2 * kP * (t + i * TPR));
+                    copy16(dst + S::kTensor, py + 2 * kP * (t + i * TPR));
+                }
+        }
+        copy_commit();
     };
-    if (kAhead) {
+    const int64_t step = (int64_t)gridDim.x * kRows, first = (int64_t)blockIdx.x * kRows + lane_row;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
-            if (t + i * TPR < nv) load_gamma(i, gm[i]);
-    }
-    Raw<T> xr[VPT], yr[VPT], xn[kAhead ? VPT : 1], yn[kAhead ? VPT : 1];
-    float mean = 0.f, rstd = 0.f, mean_n = 0.f, rstd_n = 0.f;
-    auto load = [&](int64_t row, Raw<T> *x, Raw<T> *y, float &m, float &r) {
-        if (row >= P.N) return;
-        const T *px = static_cast<const T *>(P.x) + row * P.E, *py = static_cast<const T *>(P.dy) + row * P.E;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-            if (t + i * TPR < nv) {
-                x[i].load(px + 8 * (t + i * TPR));
-                y[i].load(py + 8 * (t + i * TPR));
-            }
-        m = P.mean[row];
-        r = P.rstd[row];
-    };
-    const int64_t step = (int64_t)gridDim.x * kRows;
-    if (kAhead) load((int64_t)blockIdx.x * kRows + lane_row, xr, yr, mean, rstd);
+    for (int s = 0; s < S::kStages - 1; ++s) fetch(first + s * step, s);
+    int stage = 0;
+    float mean_n = first < P.N ? P.mean[first] : 0.f, rstd_n = first < P.N ? P.rstd[first] : 0.f;
     for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < P.N; r0 += step) {
         const int64_t row = r0 + lane_row;
         const bool live = row < P.N;
-        if (kAhead) load(row + step, xn, yn, mean_n, rstd_n);
-        else load(row, xr, yr, mean, rstd);
+        const float mean = mean_n, rstd = rstd_n;
+        if (row + step < P.N) {
+            mean_n = P.mean[row + step];
+            rstd_n = P.rstd[row + step];
+        }
+        fetch(row + (S::kStages - 1) * step, stage == 0 ? S::kStages - 1 : stage - 1);
+        copy_wait<S::kStages - 1>();
+        const uint8_t *xs = mine + stage * 2 * S::kTensor, *ys = xs + S::kTensor;
         const float2 off = both(-mean), scale = both(rstd);
         float2 p1 = both(0.f), p2 = both(0.f);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (live && t + i * TPR < nv) {
-                float2 x[4], a[4];
-                xr[i].get(x);
-                yr[i].get(a);
-                float2 (&g)[4] = gm[kAhead ? i : 0];
-                if (!kAhead) load_gamma(i, g);
+        for (int i = 0; i < CPT; ++i) {
+            if (live && t + i * TPR < chunks) {
+                float2 x[kP], a[kP];
+                take_chunk<T>(xs + i * kStep, x);
+                take_chunk<T>(ys + i * kStep, a);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < kP; ++e) {
                     const float2 xh = mul2(add2(x[e], off), scale);
                     dg[i][e] = fma2(a[e], xh, dg[i][e]);
                     db[i][e] = add2(db[i][e], a[e]);
-                    a[e] = mul2(a[e], g[e]);
+                    a[e] = mul2(a[e], gm[i][e]);
                     p1 = add2(p1, a[e]);
                     p2 = fma2(a[e], xh, p2);
                 }
@@ -410,62 +440,61 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) pe_norm_bwd_kernel(const No
         const float s2 = row_sum<TPR>(p2.x + p2.y, red) * inv_e;
         T *dx = static_cast<T *>(P.y) + row * P.E;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (live && t + i * TPR < nv) {
-                float2 x[4], a[4];
-                xr[i].get(x);
-                yr[i].get(a);
-                float2 (&g)[4] = gm[kAhead ? i : 0];
-                if (!kAhead) load_gamma(i, g);
-                float o[8];
+        for (int i = 0; i < CPT; ++i) {
+            if (live && t + i * TPR < chunks) {
+                float2 x[kP], a[kP];
+                take_chunk<T>(xs + i * kStep, x);
+                take_chunk<T>(ys + i * kStep, a);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < kP; ++e) {
                     const float2 xh = mul2(add2(x[e], off), scale);
-                    const float2 r = mul2(scale, fma2(xh, both(-s2), fma2(a[e], g[e], both(-s1))));
-                    o[2 * e] = r.x, o[2 * e + 1] = r.y;
+                    a[e] = mul2(scale, fma2(xh, both(-s2), fma2(a[e], gm[i][e], both(-s1))));
                 }
-                store8(dx + 8 * (t + i * TPR), o);
+                put_chunk<T>(dx + 2 * kP * (t + i * TPR), a);
             }
         }
-        if (kAhead) {
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) xr[i] = xn[i], yr[i] = yn[i];
-            mean = mean_n;
-            rstd = rstd_n;
-        }
+        stage = stage + 1 == S::kStages ? 0 : stage + 1;
     }
     if (!P.part) return;
-    float *out = P.part + (int64_t)blockIdx.x * 2 * P.E;
-    auto put = [&](float *dst, const float2 (&v)[4]) {
-        *reinterpret_cast<float4 *>(dst) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-        *reinterpret_cast<float4 *>(dst + 4) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
-    };
-    if constexpr (kRows > 1) {                            // the block's rows, added in order by the first
-        if (lane_row > 0) {
+    // the sums of the block's other rows go through shared memory, added in order
+    float2 *sums = reinterpret_cast<float2 *>(ring), *out = reinterpret_cast<float2 *>(P.part + (int64_t)blockIdx.x * 2 * P.E);
+    const int half = P.E / 2;
+    if constexpr (kRows > 1) {
+        copy_wait<0>();
+        for (int r = 1; r < kRows; ++r) {
+            __syncthreads();                              // the ring, or the last row's sums, are done with
+            if (lane_row == r) {
 #pragma unroll
-            for (int i = 0; i < VPT; ++i)
-                if (t + i * TPR < nv) {
-                    put(sums + (lane_row - 1) * 2 * P.E + 8 * (t + i * TPR), dg[i]);
-                    put(sums + (lane_row - 1) * 2 * P.E + P.E + 8 * (t + i * TPR), db[i]);
-                }
+                for (int i = 0; i < CPT; ++i)
+                    if (t + i * TPR < chunks)
+#pragma unroll
+                        for (int e = 0; e < kP; ++e) {
+                            sums[kP * (t + i * TPR) + e] = dg[i][e];
+                            sums[half + kP * (t + i * TPR) + e] = db[i][e];
+                        }
+            }
+            __syncthreads();
+            if (lane_row == 0) {
+#pragma unroll
+                for (int i = 0; i < CPT; ++i)
+                    if (t + i * TPR < chunks)
+#pragma unroll
+                        for (int e = 0; e < kP; ++e) {
+                            dg[i][e] = add2(dg[i][e], sums[kP * (t + i * TPR) + e]);
+                            db[i][e] = add2(db[i][e], sums[half + kP * (t + i * TPR) + e]);
+                        }
+            }
         }
-        __syncthreads();
         if (lane_row > 0) return;
     }
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        if (t + i * TPR < nv) {
-            const int e0 = 8 * (t + i * TPR);
-            for (int r = 0; r < kRows - 1; ++r) {
-                const float2 *u = reinterpret_cast<const float2 *>(sums + r * 2 * P.E + e0);
-                const float2 *w = reinterpret_cast<const float2 *>(sums + r * 2 * P.E + P.E + e0);
+    for (int i = 0; i < CPT; ++i)
+        if (t + i * TPR < chunks)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dg[i][e] = add2(dg[i][e], u[e]), db[i][e] = add2(db[i][e], w[e]);
+            for (int e = 0; e < kP; ++e) {
+                out[kP * (t + i * TPR) + e] = dg[i][e];
+                out[half + kP * (t + i * TPR) + e] = db[i][e];
             }
-            put(out + e0, dg[i]);
-            put(out + P.E + e0, db[i]);
-        }
-    }
 }
 
 // dgamma and dbeta from `n` partial rows of 2 E: a block sums 32 columns, its 32

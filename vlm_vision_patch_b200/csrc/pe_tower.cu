@@ -72,60 +72,74 @@ cudaError_t launch_rope(const RopeParams &P, cudaStream_t st) {
 
 // ------------------------------------------------------------- layer norm
 
-// Threads per row (see pe_rows.cuh).  Forward: a warp up to 1280 features, then 128
-// and 256 (fewer, fuller threads beat 1024 here: 8192 fp32 features ran at 2.5 TB/s
-// with those).  Backward: as few as its sums beside two rows leave registers for.
-int norm_tpr(int E, bool f32, bool backward) {
-    if (!backward) return E <= 1280 ? 32 : (E <= 4096 ? 128 : 256);
-    if (E <= (f32 ? 768 : 1280)) return 32;
-    if (f32 && E <= 1536) return 64;
-    return E <= (f32 ? 3072 : 4096) ? 128 : 1024;
-}
+// Forward: a warp a row up to 1280 features, then 128 and 256 threads (8192 fp32
+// features: 2.5 TB/s with 1024 threads, 5.8 with 256 fuller ones).
+int norm_fwd_tpr(int E) { return E <= 1280 ? 32 : (E <= 4096 ? 128 : 256); }
 
 int norm_rows(int tpr) { return tpr > 128 ? 1 : 128 / tpr; }          // rows per block
 
-// Blocks of the backward kernel: as many as are resident, since each writes one
-// partial row of 2 E sums.
-int norm_bwd_blocks(int64_t N, int E, bool f32, int sms) {
-    const int tpr = norm_tpr(E, f32, true), rows = norm_rows(tpr);
-    return (int)std::min<int64_t>((N + rows - 1) / rows, (int64_t)sms * (tpr == 1024 ? 1 : 2));
+// Backward: as few threads as hold the row in 5 chunks of 16 bytes each (4 beyond
+// 256 threads), so that the sums fit their registers.
+struct NormBwdPlan {
+    int tpr, cpt;
+    int blocks;                  // as many as are resident: each writes one partial row of 2 E sums
+};
+
+NormBwdPlan plan_norm_bwd(int64_t N, int E, bool f32, int sms) {
+    const int chunks = E * (f32 ? 4 : 2) / 16;
+    NormBwdPlan p = {32, 0, 0};
+    while (chunks > p.tpr * (p.tpr <= 256 ? 5 : 4)) p.tpr *= 2;
+    p.cpt = (chunks + p.tpr - 1) / p.tpr;
+    const int resident = p.tpr <= 128 ? 3 : (p.tpr == 256 && p.cpt <= 4 ? 2 : 1);
+    p.blocks = (int)std::min<int64_t>((N + norm_rows(p.tpr) - 1) / norm_rows(p.tpr), (int64_t)sms * resident);
+    return p;
 }
 
-template <class T, bool BACKWARD, int TPR, int VPT>
+template <class T, bool BACKWARD, int TPR, int PER>
 cudaError_t launch_norm(const NormParams &P, int blocks, cudaStream_t st) {
     if constexpr (!BACKWARD) {
-        pe_norm_fwd_kernel<T, TPR, VPT><<<(unsigned)blocks, kNormThreads<TPR>, 0, st>>>(P);
+        pe_norm_fwd_kernel<T, TPR, PER><<<(unsigned)blocks, kNormThreads<TPR>, 0, st>>>(P);
     } else {
-        const size_t smem = P.part ? (size_t)(kNormThreads<TPR> / TPR - 1) * 2 * P.E * sizeof(float) : 0;
-        pe_norm_bwd_kernel<T, TPR, VPT><<<(unsigned)blocks, kNormThreads<TPR>, smem, st>>>(P);
+        using S = NormBwd<TPR, PER>;
+        auto kern = pe_norm_bwd_kernel<T, TPR, PER>;
+        if (S::kSmem > 40 * 1024) {                       // 48 KB with the static part
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+            if (e != cudaSuccess) return e;
+        }
+        kern<<<(unsigned)blocks, S::kThreads, S::kSmem, st>>>(P);
     }
     return cudaGetLastError();
 }
 
-// The kernel of VPT = lo .. hi groups per thread.
+// The kernel of LO .. HI groups or chunks per thread.
 template <class T, bool BACKWARD, int TPR, int LO, int HI>
-cudaError_t pick_norm(const NormParams &P, int vpt, int blocks, cudaStream_t st) {
+cudaError_t pick_norm(const NormParams &P, int per, int blocks, cudaStream_t st) {
     if constexpr (LO < HI) {
-        if (vpt > LO) return pick_norm<T, BACKWARD, TPR, LO + 1, HI>(P, vpt, blocks, st);
+        if (per > LO) return pick_norm<T, BACKWARD, TPR, LO + 1, HI>(P, per, blocks, st);
     }
     return launch_norm<T, BACKWARD, TPR, LO>(P, blocks, st);
 }
 
-template <class T, bool BACKWARD>
-cudaError_t dispatch_norm(const NormParams &P, int blocks, cudaStream_t st) {
-    constexpr bool kF32 = sizeof(T) == 4;
-    const int tpr = norm_tpr(P.E, kF32, BACKWARD), vpt = (P.E / 8 + tpr - 1) / tpr;
-    if constexpr (!BACKWARD) {
-        if (tpr == 32) return pick_norm<T, false, 32, 1, 5>(P, vpt, blocks, st);
-        if (tpr == 128) return pick_norm<T, false, 128, 2, 4>(P, vpt, blocks, st);
-        return pick_norm<T, false, 256, 3, 8>(P, vpt, blocks, st);
-    } else {
-        if (tpr == 32) return pick_norm<T, true, 32, 1, kF32 ? 3 : 5>(P, vpt, blocks, st);
-        if constexpr (kF32)
-            if (tpr == 64) return pick_norm<T, true, 64, 2, 3>(P, vpt, blocks, st);
-        if (tpr == 128) return pick_norm<T, true, 128, 2, kF32 ? 3 : 4>(P, vpt, blocks, st);
-        return pick_norm<T, true, 1024, 1, 2>(P, vpt, blocks, st);
+template <class T>
+cudaError_t norm_forward(const NormParams &P, cudaStream_t st) {
+    const int tpr = norm_fwd_tpr(P.E), vpt = (P.E / 8 + tpr - 1) / tpr, rows = norm_rows(tpr);
+    const int blocks = (int)((P.N + rows - 1) / rows);
+    if (tpr == 32) return pick_norm<T, false, 32, 1, 5>(P, vpt, blocks, st);
+    if (tpr == 128) return pick_norm<T, false, 128, 2, 4>(P, vpt, blocks, st);
+    return pick_norm<T, false, 256, 3, 8>(P, vpt, blocks, st);
+}
+
+template <class T>
+cudaError_t norm_backward(const NormParams &P, const NormBwdPlan &p, cudaStream_t st) {
+    switch (p.tpr) {
+        case 32: return pick_norm<T, true, 32, 1, 5>(P, p.cpt, p.blocks, st);
+        case 64: return pick_norm<T, true, 64, 3, 5>(P, p.cpt, p.blocks, st);
+        case 128: return pick_norm<T, true, 128, 3, 5>(P, p.cpt, p.blocks, st);
+        case 256: return pick_norm<T, true, 256, 3, 5>(P, p.cpt, p.blocks, st);
+        case 512: return pick_norm<T, true, 512, 3, 4>(P, p.cpt, p.blocks, st);
     }
+    if constexpr (sizeof(T) == 4) return pick_norm<T, true, 1024, 3, 4>(P, p.cpt, p.blocks, st);
+    return cudaErrorInvalidValue;                         // bf16 rows end at 512 threads
 }
 
 pe_status check_norm(pe_dtype dt, pe_dtype w_dt, int64_t N, int E) {
@@ -347,16 +361,14 @@ pe_status pe_layernorm_forward(const void *x, pe_dtype dt, int64_t N, int E, con
     P.E = E;
     P.w_f32 = w_dt == PE_F32;
     P.eps = eps;
-    const int rows = norm_rows(norm_tpr(E, dt == PE_F32, false)), blocks = (int)((N + rows - 1) / rows);
     cudaStream_t st = (cudaStream_t)stream;
-    return finish(dt == PE_F32 ? dispatch_norm<float, false>(P, blocks, st)
-                               : dispatch_norm<__nv_bfloat16, false>(P, blocks, st));
+    return finish(dt == PE_F32 ? norm_forward<float>(P, st) : norm_forward<__nv_bfloat16>(P, st));
 }
 
 int64_t pe_layernorm_backward_workspace(int64_t N, int E) {
     if (check_norm(PE_F32, PE_F32, N, E) != PE_OK) return -1;
     const int sms = current_sms();
-    return (int64_t)std::max(norm_bwd_blocks(N, E, false, sms), norm_bwd_blocks(N, E, true, sms)) * 2 * E *
+    return (int64_t)std::max(plan_norm_bwd(N, E, false, sms).blocks, plan_norm_bwd(N, E, true, sms).blocks) * 2 * E *
            (int64_t)sizeof(float);
 }
 
@@ -372,10 +384,10 @@ pe_status pe_layernorm_backward(const void *dy, const void *x, pe_dtype dt, int6
     if (!aligned_to(mean, 4) || !aligned_to(rstd, 4)) return PE_ERR_ALIGN;
     const int sms = current_sms();
     if (sms < 1) return PE_ERR_CUDA;
-    const int blocks = norm_bwd_blocks(N, E, dt == PE_F32, sms);
+    const NormBwdPlan plan = plan_norm_bwd(N, E, dt == PE_F32, sms);
     if (dgamma && N > 0) {
         if (!ws) return PE_ERR_INVALID_ARG;
-        if (ws_bytes < (int64_t)blocks * 2 * E * (int64_t)sizeof(float)) return PE_ERR_SHAPE;
+        if (ws_bytes < (int64_t)plan.blocks * 2 * E * (int64_t)sizeof(float)) return PE_ERR_SHAPE;
     }
     NormParams P;
     std::memset(&P, 0, sizeof(P));
@@ -391,12 +403,11 @@ pe_status pe_layernorm_backward(const void *dy, const void *x, pe_dtype dt, int6
     P.w_f32 = w_dt == PE_F32;
     cudaStream_t st = (cudaStream_t)stream;
     if (N > 0) {
-        const cudaError_t e = dt == PE_F32 ? dispatch_norm<float, true>(P, blocks, st)
-                                           : dispatch_norm<__nv_bfloat16, true>(P, blocks, st);
+        const cudaError_t e = dt == PE_F32 ? norm_backward<float>(P, plan, st) : norm_backward<__nv_bfloat16>(P, plan, st);
         if (e != cudaSuccess) return PE_ERR_CUDA;
     }
     if (!dgamma) return PE_OK;
-    pe_norm_sum_kernel<<<(2 * E + 31) / 32, 1024, 0, st>>>(P.part, blocks, E, P.w_f32, dgamma, dbeta);
+    pe_norm_sum_kernel<<<(2 * E + 31) / 32, 1024, 0, st>>>(P.part, plan.blocks, E, P.w_f32, dgamma, dbeta);
     return finish(cudaGetLastError());
 }
 
