@@ -138,7 +138,9 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, sections
     qs = _heads(q, "q", dev, dtype, shape)
     if out_q is None:
         out_q = q.new_empty(shape)
-    qo = _heads(out_q, "out_q", dev, dtype, shape)
+        qo = B.pe_heads(out_q.data_ptr(), hq * d, d)
+    else:
+        qo = _heads(out_q, "out_q", dev, dtype, shape)
     hk, ks, ko = 0, _NONE, _NONE
     if k is not None:
         hk = k.shape[1]
@@ -146,21 +148,22 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, sections
         ks = _heads(k, "k", dev, dtype, k_shape)
         if out_k is None:
             out_k = k.new_empty(k_shape)
-        ko = _heads(out_k, "out_k", dev, dtype, k_shape)
+            ko = B.pe_heads(out_k.data_ptr(), hk * d, d)
+        else:
+            ko = _heads(out_k, "out_k", dev, dtype, k_shape)
     B.pe_rope(qs, ks, dt, n, hq, hk, d, pos_ptr, sections, theta, axial, inverse, qo, ko, _raw(dev))
     return out_q, out_k if k is not None else None
 
 
-def _weights(dev: int, E: int, **weights) -> Tuple[list, int]:
-    """Pointers of the optional [E] weights, which share one dtype."""
-    ptrs, dtype = [], None
-    for name, w in weights.items():
-        ptrs.append(None if w is None else _dense(w, name, dev, (E,)))
-        if w is not None:
-            if dtype is not None and w.dtype != dtype:
-                raise TypeError("the weights must share one dtype")
-            dtype = w.dtype
-    return ptrs, B.PE_F32 if dtype is None else _dt(dtype)
+def _weights(dev: int, E: int, gamma, beta=None) -> Tuple[Optional[int], Optional[int], int]:
+    """Pointers of the optional [E] weights, and their dtype."""
+    if gamma is not None and beta is not None and beta.dtype != gamma.dtype:
+        raise TypeError("the weights must share one dtype")
+    g = None if gamma is None else _dense(gamma, "gamma", dev, (E,))
+    b = None if beta is None else _dense(beta, "beta", dev, (E,))
+    if gamma is not None:
+        return g, b, _dt(gamma.dtype)
+    return g, b, B.PE_F32 if beta is None else _dt(beta.dtype)
 
 
 def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
@@ -176,11 +179,14 @@ def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Opti
         raise ValueError("x must be [..., E]")
     shape = x.shape
     E, lead = shape[-1], shape[:-1]
-    xp, dt = _dense(x, "x", dev), _dt(x.dtype)
-    (g, b), w_dt = _weights(dev, E, gamma=gamma, beta=beta)
+    dtype = x.dtype
+    xp, dt = _dense(x, "x", dev), _dt(dtype)
+    g, b, w_dt = _weights(dev, E, gamma, beta)
     if out is None:
-        out = torch.empty_like(x)
-    op = _dense(out, "out", dev, shape, x.dtype)
+        out = x.new_empty(shape)
+        op = out.data_ptr()
+    else:
+        op = _dense(out, "out", dev, shape, dtype)
     mean = rstd = mp = rp = None
     if stats:
         mean, rstd = x.new_empty(lead, dtype=_F32), x.new_empty(lead, dtype=_F32)
@@ -207,19 +213,21 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch
     xp, dt = _dense(x, "x", dev), _dt(x.dtype)
     dp = _dense(dy, "dy", dev, shape, x.dtype)
     mp, rp = _dense(mean, "mean", dev, lead, _F32), _dense(rstd, "rstd", dev, lead, _F32)
-    (g,), w_dt = _weights(dev, E, gamma=gamma)
+    g, _, w_dt = _weights(dev, E, gamma)
     if weight_dtype is not None:
         if gamma is not None and weight_dtype != gamma.dtype:
             raise TypeError("weight_dtype must be gamma's dtype")
         w_dt = _dt(weight_dtype)
     if out is None:
-        out = torch.empty_like(x)
-    op = _dense(out, "out", dev, shape, x.dtype)
+        out = x.new_empty(shape)
+        op = out.data_ptr()
+    else:
+        op = _dense(out, "out", dev, shape, x.dtype)
     dgamma = dbeta = gp = bp = ws = None
     nbytes = 0
     if weight_grads:
         dgamma = x.new_empty(E, dtype=_F32 if w_dt == B.PE_F32 else _BF16)
-        dbeta = torch.empty_like(dgamma)
+        dbeta = dgamma.new_empty(E)
         nbytes = B.pe_layernorm_backward_workspace(n, E)
         scratch = x.new_empty(max(nbytes, 0), dtype=torch.uint8)
         gp, bp, ws = dgamma.data_ptr(), dbeta.data_ptr(), scratch.data_ptr()
@@ -259,6 +267,11 @@ class Attention:
             raise ValueError("q, k and v must be [rows, heads, head_dim]")
         return (q.shape[0], self.heads, self.head_dim), (k.shape[0], self.kv_heads, self.head_dim)
 
+    @staticmethod
+    def _fresh(t, shape):
+        """A tensor this module has just allocated: dense, nothing to check."""
+        return B.pe_heads(t.data_ptr(), shape[1] * shape[2], shape[2])
+
     def _workspace(self, q, n, nq, nk, backward):
         """(tensor or None, pointer or None, bytes)"""
         nbytes = B.pe_attention_workspace(self.h, n, nq, nk, backward)
@@ -283,9 +296,12 @@ class Attention:
         qs, ks, vs = _heads(q, "q", d, _BF16, sq), _heads(k, "k", d, _BF16, sk), _heads(v, "v", d, _BF16, sk)
         if out is None:
             out = q.new_empty(sq)
+            os = self._fresh(out, sq)
+        else:
+            os = _heads(out, "out", d, _BF16, sq)
         stat = q.new_empty((self.heads, sq[0]), dtype=_F32) if lse else None
         ws, wp, nbytes = self._workspace(q, n, sq[0], sk[0], False)
-        B.pe_attention_forward(self.h, n, cq, sq[0], ck, sk[0], qs, ks, vs, _heads(out, "out", d, _BF16, sq),
+        B.pe_attention_forward(self.h, n, cq, sq[0], ck, sk[0], qs, ks, vs, os,
                                stat.data_ptr() if lse else None, wp, nbytes, _raw(d))
         return out, stat
 
@@ -304,14 +320,17 @@ class Attention:
         lp = _dense(lse, "lse", d, (self.heads, sq[0]), _F32)
         args = [_heads(t, name, d, _BF16, s) for t, name, s in
                 ((q, "q", sq), (k, "k", sk), (v, "v", sk), (out, "out", sq), (dout, "dout", sq))]
-        dq = q.new_empty(sq) if dq is None else dq
-        dk = k.new_empty(sk) if dk is None else dk
-        dv = k.new_empty(sk) if dv is None else dv
+        grads = []
+        for t, name, s in ((dq, "dq", sq), (dk, "dk", sk), (dv, "dv", sk)):
+            if t is None:
+                t = q.new_empty(s)
+                grads.append((t, self._fresh(t, s)))
+            else:
+                grads.append((t, _heads(t, name, d, _BF16, s)))
         ws, wp, nbytes = self._workspace(q, n, sq[0], sk[0], True)
         B.pe_attention_backward(self.h, n, cq, sq[0], ck, sk[0], args[0], args[1], args[2], args[3], lp, args[4],
-                                _heads(dq, "dq", d, _BF16, sq), _heads(dk, "dk", d, _BF16, sk),
-                                _heads(dv, "dv", d, _BF16, sk), wp, nbytes, _raw(d))
-        return dq, dk, dv
+                                grads[0][1], grads[1][1], grads[2][1], wp, nbytes, _raw(d))
+        return grads[0][0], grads[1][0], grads[2][0]
 
     def last_error(self) -> int:
         return B.pe_attention_last_error(self.h)
