@@ -217,14 +217,14 @@ struct Work {
 // n / rows + n_seq tiles.
 __device__ __forceinline__ Work find_work(const AttnParams &P, bool by_key, int t, int rows) {
     const int lane = threadIdx.x & 31;
-    const int32_t *cu = by_key ? P.cu_k : P.cu_q;
-    const int n = by_key ? P.Nk : P.Nq;
     Work w = {0, 0, 0, 0, -1};
     for (int base = 0; base < P.n_seq; base += 32) {
         const int s = base + lane;
-        int tiles = 0;
+        int q0 = 0, q1 = 0, k0 = 0, k1 = 0, tiles = 0;     // both sides at once: one trip to memory
         if (s < P.n_seq) {
-            const int len = boundary(cu, s + 1, n) - boundary(cu, s, n);
+            q0 = boundary(P.cu_q, s, P.Nq), q1 = boundary(P.cu_q, s + 1, P.Nq);
+            k0 = boundary(P.cu_k, s, P.Nk), k1 = boundary(P.cu_k, s + 1, P.Nk);
+            const int len = by_key ? k1 - k0 : q1 - q0;
             tiles = len > 0 ? (len + rows - 1) / rows : 0;
         }
         int sum = tiles;
@@ -235,19 +235,29 @@ __device__ __forceinline__ Work find_work(const AttnParams &P, bool by_key, int 
         }
         const unsigned hit = __ballot_sync(0xffffffffu, t < sum);
         if (hit) {
-            const int src = __ffs(hit) - 1, seq = base + src;
-            const int before = __shfl_sync(0xffffffffu, sum - tiles, src);
-            w.q0 = boundary(P.cu_q, seq, P.Nq);
-            w.lq = max(boundary(P.cu_q, seq + 1, P.Nq) - w.q0, 0);
-            w.k0 = boundary(P.cu_k, seq, P.Nk);
-            w.lk = max(boundary(P.cu_k, seq + 1, P.Nk) - w.k0, 0);
-            w.row = (t - before) * rows;
+            const int src = __ffs(hit) - 1;
+            w.q0 = __shfl_sync(0xffffffffu, q0, src);
+            w.lq = __shfl_sync(0xffffffffu, max(q1 - q0, 0), src);
+            w.k0 = __shfl_sync(0xffffffffu, k0, src);
+            w.lk = __shfl_sync(0xffffffffu, max(k1 - k0, 0), src);
+            w.row = (t - __shfl_sync(0xffffffffu, sum - tiles, src)) * rows;
             return w;
         }
         t -= __shfl_sync(0xffffffffu, sum, 31);
     }
     return w;
 }
+
+// A place in a ring of N stages, and the parity of its barriers' phase there.
+template <int N>
+struct Slot {
+    int at = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int by = 1) {
+        at += by;
+        if (at >= N) at -= N, phase ^= 1;
+    }
+};
 
 // Keys that query row i of a sequence sees.
 __device__ __forceinline__ int keys_seen(const AttnParams &P, const Work &w, int i) {
@@ -479,6 +489,7 @@ __device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, con
 // Joins the parts of a row and head (one warp each): out = sum_z w_z out_z / sum_z
 // w_z with w_z = 2^(lse2_z - max).
 __global__ void __launch_bounds__(256) pe_attn_join_kernel(const __grid_constant__ AttnParams P) {
+    griddep_wait();
     const int lane = threadIdx.x & 31;
     const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);          // [Hq, Nq]
     if (at >= (int64_t)P.Hq * P.Nq) return;
@@ -490,16 +501,22 @@ __global__ void __launch_bounds__(256) pe_attn_join_kernel(const __grid_constant
     }
     if (lo < 0 || r >= boundary(P.cu_q, lo + 1, P.Nq)) return;                // a row of no sequence
     const int64_t step = (int64_t)P.Hq * P.Nq;
-    float top = -INFINITY;
-    for (int z = 0; z < P.splits; ++z) top = fmaxf(top, P.part_lse2[z * step + at]);
+    // at most 64 parts: a lane holds two of their statistics
+    const float l0 = lane < P.splits ? P.part_lse2[lane * step + at] : -INFINITY;
+    const float l1 = lane + 32 < P.splits ? P.part_lse2[(lane + 32) * step + at] : -INFINITY;
+    float top = fmaxf(l0, l1);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // a part that saw no key weighs nothing, and what its place holds is not read
+    const float w0 = l0 == -INFINITY ? 0.f : ex2(l0 - top), w1 = l1 == -INFINITY ? 0.f : ex2(l1 - top);
+    float sum = w0 + w1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
+#pragma unroll 8
     for (int z = 0; z < P.splits; ++z) {
-        const float l = P.part_lse2[z * step + at];
-        if (l == -INFINITY) continue;                     // saw no key
-        const float w = ex2(l - top);
-        sum += w;
-        if (4 * lane < P.D) {
+        const float w = __shfl_sync(0xffffffffu, z < 32 ? w0 : w1, z & 31);
+        if (w != 0.f && 4 * lane < P.D) {
             const float4 v = *reinterpret_cast<const float4 *>(P.part_out + (z * step + at) * P.D + 4 * lane);
             o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
         }
@@ -530,11 +547,12 @@ __device__ __forceinline__ void fwd_load(const AttnParams &P, FwdBars &B, const 
     }
     int f = 0;
     bool ok = true;
-    for (; f < 2 * n_max; ++f) {
-        const int slot = f % S::kStages;
+    Slot<S::kStages> r;
+    for (; f < 2 * n_max; ++f, r.next()) {
+        const int slot = r.at;
         const bool is_v = f == 2 * n_max - 1 || (f > 0 && !(f & 1));
         const int j = f == 2 * n_max - 1 ? n_max - 1 : (is_v ? (f >> 1) - 1 : (f + 1) >> 1);
-        ok = warp_wait(&B.empty[slot], ((f / S::kStages) & 1) ^ 1, abort);
+        ok = warp_wait(&B.empty[slot], r.phase ^ 1, abort);
         if (!ok) break;
         uint8_t *dst = ring + slot * S::kKv;
         const int valid = min(w.lk - kb - j * KT, KT);
@@ -580,46 +598,46 @@ __device__ __forceinline__ void fwd_mma(FwdBars &B, const Work &w, uint8_t *sq, 
     const uint32_t d_q = desc_k(smem_addr(sq)) + t * (S::kQ >> 4), d_k = desc_k(smem_addr(ring));
     const uint32_t d_v = desc_mn<S::kChunk>(smem_addr(ring));
     const uint32_t ts = tm + S::kColS + t * KT, tp = tm + S::kColP + t * (KT / 2), to = tm + S::kColO + t * DP;
-    auto slot_of = [](int f) { return (uint32_t)(f % S::kStages) * (S::kKv >> 4); };
-    auto wait_full = [&](int f) { return warp_wait(&B.full[f % S::kStages], (f / S::kStages) & 1, abort); };
-    auto issue_s = [&](int f) {
-        const uint32_t b = d_k + slot_of(f);
+    Slot<S::kStages> r;                                     // K0 K1 V0 K2 V1 ... in the order of the loads
+    auto wait_full = [&] { return warp_wait(&B.full[r.at], r.phase, abort); };
+    auto issue_s = [&] {
+        const uint32_t b = d_k + r.at * (S::kKv >> 4);
         if (one) {
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k)
                 mma_ss(ts, d_q + step_k<kChunkBytes>(k), b + step_k<S::kChunk>(k), kDescHi, kDescHi, kIdS, k > 0);
             mma_commit(&B.s_full[t]);
-            mma_commit(&B.empty[f % S::kStages]);
+            mma_commit(&B.empty[r.at]);
         }
         __syncwarp();
     };
-    // a tile that needs none of the keys at f gives the slot back at once
-    auto skip = [&](int f) {
-        if (one) mbar_arrive(smem_addr(&B.empty[f % S::kStages]));
+    // a tile that needs none of these keys gives the slot back at once
+    auto skip = [&] {
+        if (one) mbar_arrive(smem_addr(&B.empty[r.at]));
         __syncwarp();
     };
-    bool ok = n_max == 0 || (warp_wait(&B.qfull, 0, abort) && wait_full(0));
+    bool ok = n_max == 0 || (warp_wait(&B.qfull, 0, abort) && wait_full());
     if (ok && n_max > 0) {
         tc_fence_after();
-        if (n > 0) issue_s(0);
-        else skip(0);
+        if (n > 0) issue_s();
+        else skip();
+        r.next();
     }
     for (int j = 0; j < n_max && ok; ++j) {
-        const bool more = j + 1 < n_max;
-        const int fk = 2 * j + 1, fv = more ? 2 * j + 2 : 2 * j + 1;
-        if (more) {                                         // the next scores, once the last have been read
-            ok = wait_full(fk) && (j + 1 >= n || warp_wait(&B.s_free[t], j & 1, abort));
+        if (j + 1 < n_max) {                                // the next scores, once the last have been read
+            ok = wait_full() && (j + 1 >= n || warp_wait(&B.s_free[t], j & 1, abort));
             if (!ok) break;
             tc_fence_after();
-            if (j + 1 < n) issue_s(fk);
-            else skip(fk);
+            if (j + 1 < n) issue_s();
+            else skip();
+            r.next();
         }
-        ok = wait_full(fv) && (j >= n || warp_wait(&B.p_full[t], j & 1, abort));
+        ok = wait_full() && (j >= n || warp_wait(&B.p_full[t], j & 1, abort));
         if (!ok) break;
         tc_fence_after();
         if (j < n) {
             const int steps = (min(w.lk - kb - j * KT, KT) + 15) / 16;
-            const uint32_t b = d_v + slot_of(fv);
+            const uint32_t b = d_v + r.at * (S::kKv >> 4);
             if (one) {
                 mma_ts(to, tp, b, kDescHi, kIdO, j > 0);
                 if (steps == KT / 16) {
@@ -629,12 +647,13 @@ __device__ __forceinline__ void fwd_mma(FwdBars &B, const Work &w, uint8_t *sq, 
                     for (int k = 1; k < steps; ++k) mma_ts(to, tp + 8 * k, b + step_mn(k), kDescHi, kIdO, true);
                 }
                 mma_commit(&B.pv_done[t]);
-                mma_commit(&B.empty[fv % S::kStages]);
+                mma_commit(&B.empty[r.at]);
             }
             __syncwarp();
         } else {
-            skip(fv);
+            skip();
         }
+        r.next();
     }
     if (!ok) drain_mmas(one, &B.drain[t]);
 }
@@ -674,9 +693,6 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             prefetch_tmap(&mv);
         }
     }
-    __syncthreads();
-    const Work w = B.w;
-    if (w.row < 0) return;
     if (warp == 8) {
         tmem_alloc(smem_addr(&B.tmem), 512);
         tmem_relinquish();
@@ -684,6 +700,12 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    const Work w = B.w;
+    if (P.splits > 1) griddep_launch_dependents();          // the joining kernel
+    if (w.row < 0) {                                        // more blocks than tiles
+        if (warp == 8) tmem_dealloc(B.tmem, 512);
+        return;
+    }
     // key tiles that each query tile meets (the second tile may be missing) ...
     auto tiles_of = [&](int t) {
         const int last = min(w.row + (t + 1) * rows, w.lq) - 1;
@@ -737,18 +759,27 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
 
 constexpr int kStream = 64;                       // streamed rows per tile
 constexpr int kStreamChunk = kStream * 128;       // bytes of 64 rows of 64 bf16
-constexpr int kBwdStages = 4;
+constexpr uint32_t kSelect = kTile * 32, kStats = kStream * 16;
 
-template <int DP>
-constexpr uint32_t kBwdTiles = kChunks<DP> * (2 * kChunkBytes + kBwdStages * 2 * kStreamChunk);
-// Behind the tiles: the two selectors of the statistics (128 rows of 16 bf16), the
-// statistics of each stage's 64 queries (8 bf16), and 64 rows of zeros.
-constexpr uint32_t kSelect = kTile * 32, kStats = kStream * 16, kExtra = 2 * kSelect + (kBwdStages + 1) * kStats;
-template <int DP>
-constexpr size_t kBwdSmem = (size_t)kBwdTiles<DP> + kExtra + 1024;
+// Shared memory: the kept tiles, the ring, and for keys the two selectors of the
+// statistics (128 rows of 16 bf16), the statistics of each stage's 64 queries
+// (8 bf16) and 64 rows of zeros.  A stage lives from its load until the sums have
+// read it, some three tiles' time, so the ring is as deep as fits in 212 KB (head
+// size 64: 8 stages, 1186 us for 4 x 4096 rows against 1271 with 4).  The rest is
+// left to L1: a fifth stage at head size 80 took the dq kernel from 669 to 743 us.
+template <int DP, bool KEYS>
+struct BwdShape {
+    static constexpr uint32_t kKept = kChunks<DP> * kChunkBytes, kOne = kChunks<DP> * kStreamChunk;
+    static constexpr uint32_t kFixed = 1024 + 2 * kKept + (KEYS ? 2 * kSelect + kStats : 0);
+    static constexpr uint32_t kStage = 2 * kOne + (KEYS ? kStats : 0);
+    static constexpr int kFit = (212 * 1024 - kFixed) / kStage, kStages = kFit < 8 ? kFit : 8;
+    static constexpr uint32_t kTiles = 2 * kKept + kStages * 2 * kOne;
+    static constexpr size_t kSmem = kFixed + (size_t)kStages * kStage;
+};
+constexpr int kBwdMaxStages = 8;
 
 struct BwdBars {
-    uint64_t full[kBwdStages], empty[kBwdStages], tail, xfull, s_full[2], s_free[2], d_full[2], acc_done[2], acc_full, drain[3];
+    uint64_t full[kBwdMaxStages], empty[kBwdMaxStages], tail, xfull, s_full[2], s_free[2], d_full[2], acc_done[2], acc_full, drain[3];
     uint32_t tmem;
     int abort;
     Work w;
@@ -839,11 +870,14 @@ __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const
         }
     }
     const int shift = w.lk - w.lq;
-    for (int j = g; j < st.n; j += 2) {
+    int tile = g;                                           // of the current head's streamed tiles
+    for (int j = g; j < st.n; j += 2, tile += 2) {
         const int n = j >> 1;
+        if (KEYS)
+            while (tile >= st.per_head) tile -= st.per_head;
         if (!warp_wait(&B.s_full[g], n & 1, abort)) return;
         tc_fence_after();
-        const int y = (st.first + (KEYS ? j % st.per_head : j)) * kStream;      // first streamed row
+        const int y = (st.first + tile) * kStream;          // first streamed row
         uint32_t s[4][16], d[4][16];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -925,8 +959,9 @@ template <int DP, bool KEYS>
 __device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const Work &w, const Stream &st,
                                          const CUtensorMap &mx0, const CUtensorMap &mx1, const CUtensorMap &my0,
                                          const CUtensorMap &my1, uint8_t *kept, uint8_t *ring, uint8_t *stats, int h) {
+    using S = BwdShape<DP, KEYS>;
     constexpr int kC = kChunks<DP>;
-    constexpr uint32_t kKept = kC * kChunkBytes, kOne = kC * kStreamChunk;     // bytes of one kept / streamed tile
+    constexpr uint32_t kKept = S::kKept, kOne = S::kOne;                       // bytes of one kept / streamed tile
     volatile int *abort = &B.abort;
     const int lane = threadIdx.x & 31, share = P.Hq / P.Hkv;
     const int y_len = KEYS ? w.lq : w.lk;                   // streamed rows of the sequence
@@ -939,14 +974,15 @@ __device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const 
                     tma_load_3d(smem_addr(kept + t * kKept + c * kChunkBytes + half * kStreamChunk), t ? &mx1 : &mx0,
                                 smem_addr(&B.xfull), 64 * c, h, x_row + half * kStream);
     }
-    int f = 0, tails = 0;
+    int f = 0, tails = 0, tile = 0, y_head = KEYS ? h * share : h / share;
     bool ok = true;
-    for (; f < st.n; ++f) {
-        const int slot = f % kBwdStages;
-        ok = warp_wait(&B.empty[slot], ((f / kBwdStages) & 1) ^ 1, abort);
+    Slot<S::kStages> r;
+    for (; f < st.n; ++f, ++tile, r.next()) {
+        const int slot = r.at;
+        ok = warp_wait(&B.empty[slot], r.phase ^ 1, abort);
         if (!ok) break;
-        const int row = (st.first + (KEYS ? f % st.per_head : f)) * kStream;
-        const int y_head = KEYS ? h * share + f / st.per_head : h / share;
+        if (KEYS && tile == st.per_head) tile = 0, ++y_head;
+        const int row = (st.first + tile) * kStream;
         const int y_row = (KEYS ? w.q0 : w.k0) + row;
         const int valid = min(y_len - row, kStream);
         uint8_t *dst = ring + slot * 2 * kOne;
@@ -981,7 +1017,7 @@ __device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const 
     }
     if (!ok) {   // a wait gave up: the copies in flight still land before the block ends
         warp_drain(&B.xfull, 0);
-        for (int s = max(f - kBwdStages, 0); s < f; ++s) warp_drain(&B.full[s % kBwdStages], (s / kBwdStages) & 1);
+        for (int s = max(f - S::kStages, 0); s < f; ++s) warp_drain(&B.full[s % S::kStages], (s / S::kStages) & 1);
     }
 }
 
@@ -991,15 +1027,17 @@ template <int DP, bool KEYS>
 __device__ __forceinline__ void bwd_scores(BwdBars &B, const Stream &st, uint8_t *kept, uint8_t *ring, uint8_t *select,
                                            uint8_t *stats, int b) {
     using T = BwdCols<DP, KEYS>;
-    constexpr int kC = kChunks<DP>;
-    constexpr uint32_t kKept = kC * kChunkBytes, kOne = kC * kStreamChunk, kIdS = idesc_bf16_f32(kTile, kStream);
+    using S = BwdShape<DP, KEYS>;
+    constexpr uint32_t kKept = S::kKept, kOne = S::kOne, kIdS = idesc_bf16_f32(kTile, kStream);
     volatile int *abort = &B.abort;
     const uint32_t one = elect_one(), tm = B.tmem;
     const uint32_t x0 = desc_k(smem_addr(kept)), x1 = desc_k(smem_addr(kept + kKept));
     bool ok = warp_wait(&B.xfull, 0, abort);
-    for (int j = b; j < st.n && ok; j += 2) {
-        const int n = j >> 1, slot = j % kBwdStages;
-        ok = warp_wait(&B.full[slot], (j / kBwdStages) & 1, abort) && (n == 0 || warp_wait(&B.s_free[b], (n - 1) & 1, abort));
+    Slot<S::kStages> r;
+    r.at = b;
+    for (int j = b; j < st.n && ok; j += 2, r.next(2)) {
+        const int n = j >> 1, slot = r.at;
+        ok = warp_wait(&B.full[slot], r.phase, abort) && (n == 0 || warp_wait(&B.s_free[b], (n - 1) & 1, abort));
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tm + b * T::kBuf, y0 = desc_k(smem_addr(ring + slot * 2 * kOne)), y1 = y0 + (kOne >> 4);
@@ -1011,7 +1049,7 @@ __device__ __forceinline__ void bwd_scores(BwdBars &B, const Stream &st, uint8_t
             for (int k = 0; k < DP / 16; ++k)
                 mma_ss(d + 64, x1 + step_k<kChunkBytes>(k), y1 + step_k<kStreamChunk>(k), kDescHi, kDescHi, kIdS, k > 0);
             if (KEYS) {
-                const uint32_t at = smem_addr(stats + slot * kStats), zeros = smem_addr(stats + kBwdStages * kStats);
+                const uint32_t at = smem_addr(stats + slot * kStats), zeros = smem_addr(stats + S::kStages * kStats);
                 const uint32_t z = desc_flat(at, zeros - at), sel = desc_flat(smem_addr(select), kTile * 16);
                 mma_ss(d, sel, z, kDescHiFlat, kDescHiFlat, kIdS, true);
                 mma_ss(d + 64, sel + (kSelect >> 4), z, kDescHiFlat, kDescHiFlat, kIdS, true);
@@ -1027,7 +1065,8 @@ __device__ __forceinline__ void bwd_scores(BwdBars &B, const Stream &st, uint8_t
 template <int DP, bool KEYS>
 __device__ __forceinline__ void bwd_sums(BwdBars &B, const Stream &st, uint8_t *ring, int y_len) {
     using T = BwdCols<DP, KEYS>;
-    constexpr uint32_t kOne = kChunks<DP> * kStreamChunk, kIdA = idesc_b_mn(kTile, DP);
+    using S = BwdShape<DP, KEYS>;
+    constexpr uint32_t kOne = S::kOne, kIdA = idesc_b_mn(kTile, DP);
     volatile int *abort = &B.abort;
     const uint32_t one = elect_one(), tm = B.tmem;
     // kept rows += A (tensor memory) times the streamed tile at z
@@ -1041,10 +1080,13 @@ __device__ __forceinline__ void bwd_sums(BwdBars &B, const Stream &st, uint8_t *
         }
     };
     bool ok = true;
-    for (int j = 0; j < st.n && ok; ++j) {
-        const int b = j & 1, slot = j % kBwdStages, row = (st.first + (KEYS ? j % st.per_head : j)) * kStream;
+    Slot<S::kStages> r;
+    int tile = 0;
+    for (int j = 0; j < st.n && ok; ++j, ++tile, r.next()) {
+        if (KEYS && tile == st.per_head) tile = 0;
+        const int b = j & 1, slot = r.at, row = (st.first + tile) * kStream;
         const int steps = (min(y_len - row, kStream) + 15) / 16;
-        ok = warp_wait(&B.full[slot], (j / kBwdStages) & 1, abort) && warp_wait(&B.d_full[b], (j >> 1) & 1, abort);
+        ok = warp_wait(&B.full[slot], r.phase, abort) && warp_wait(&B.d_full[b], (j >> 1) & 1, abort);
         if (!ok) break;
         tc_fence_after();
         const uint32_t z0 = desc_mn<kStreamChunk>(smem_addr(ring + slot * 2 * kOne)), z1 = z0 + (kOne >> 4);
@@ -1066,10 +1108,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constant__ CUtensorMap mx1,
                    const __grid_constant__ CUtensorMap my0, const __grid_constant__ CUtensorMap my1,
                    const __grid_constant__ AttnParams P) {
+    using S = BwdShape<DP, KEYS>;
     extern __shared__ uint8_t raw[];
     __shared__ BwdBars B;
-    uint8_t *kept = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023), *ring = kept + 2 * kChunks<DP> * kChunkBytes;
-    uint8_t *select = kept + kBwdTiles<DP>, *stats = select + 2 * kSelect;
+    uint8_t *kept = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023), *ring = kept + 2 * S::kKept;
+    uint8_t *select = kept + S::kTiles, *stats = select + 2 * kSelect;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.y;
     if (warp == 9) {
@@ -1077,7 +1120,7 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
         if (lane == 0) {
             B.w = w;
             B.abort = 0;
-            for (int i = 0; i < kBwdStages; ++i) {
+            for (int i = 0; i < S::kStages; ++i) {
                 mbar_init(smem_addr(&B.full[i]), 1);
                 mbar_init(smem_addr(&B.empty[i]), 1);
             }
@@ -1098,12 +1141,13 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
             prefetch_tmap(&my1);
         }
     }
-    __syncthreads();
-    const Work w = B.w;
-    if (w.row < 0) return;
+    if (warp == 8) {
+        tmem_alloc(smem_addr(&B.tmem), 512);
+        tmem_relinquish();
+    }
     if (KEYS) {
         // 1 in columns 0, 1, 2 selects the first statistic, in 4, 5, 6 the second; the rest is 0
-        for (int i = threadIdx.x; i < (int)(kExtra / 16); i += blockDim.x) {
+        for (int i = threadIdx.x; i < (int)((2 * kSelect + (S::kStages + 1) * kStats) / 16); i += blockDim.x) {
             const uint32_t one2 = 0x3F803F80u, one1 = 0x00003F80u;
             uint4 v = make_uint4(0, 0, 0, 0);
             if (i < kTile) v = make_uint4(one2, one1, 0, 0);
@@ -1112,13 +1156,17 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
         }
         fence_proxy_async_smem();
     }
-    if (warp == 8) {
-        tmem_alloc(smem_addr(&B.tmem), 512);
-        tmem_relinquish();
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    const Work w = B.w;
+    // the key kernel starts as the query kernel, whose statistics it reads, ends
+    if (!KEYS) griddep_launch_dependents();
+    if (KEYS && warp == 8) griddep_wait();
+    if (w.row < 0) {                                        // more blocks than tiles
+        if (warp == 8) tmem_dealloc(B.tmem, 512);
+        return;
+    }
     const Stream st = stream_of<KEYS>(P, w);
     if (warp < 8) {
         regs_up<224>();

@@ -209,6 +209,23 @@ bool ready_to_launch(Kernel kern, size_t smem, int dev, std::atomic<uint64_t> &d
     return true;
 }
 
+// A kernel that waits (griddepcontrol) for the one before it on the stream: its
+// blocks may start, and its set-up run, as that one's last blocks end.
+template <class... K, class... A>
+cudaError_t launch_after(void (*kern)(K...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Tiles of `rows` rows that n rows in n_seq sequences can make, at most.
 unsigned max_tiles(int64_t n, int n_seq, int rows) { return (unsigned)(n / rows + std::min<int64_t>(n_seq, n)); }
 
@@ -232,13 +249,14 @@ FwdPlan plan_forward(const pe_attention *a, int n_seq, int64_t Nq, int64_t Nk) {
     p.pack = share > 1 && share <= kTile && Nq * share <= (int64_t)kTile * n_seq ? share : 1;
     p.blocks = max_tiles(Nq, n_seq, 2 * (kTile / p.pack));
     p.rows = (unsigned)(p.pack > 1 ? a->Hkv : a->Hq);
-    // With blocks for less than a quarter of the SMs the key axis is divided until
-    // there are two a SM, but into no less than 4 tiles of an average sequence.
-    const int64_t blocks = (int64_t)std::min<int64_t>(p.blocks, Nq) * p.rows;
+    // With blocks for less than a quarter of the SMs the key axis is divided until there
+    // is one a SM, but into no less than 4 tiles of an average sequence.
+    const int rows = 2 * (kTile / p.pack);
+    const int64_t blocks = std::max<int64_t>((Nq + rows - 1) / rows, std::min<int64_t>(n_seq, Nq)) * p.rows;
     const int64_t tiles = Nk / n_seq / 128;
     p.splits = 1;
     if (blocks * 4 <= a->num_sms)
-        p.splits = (int)std::max<int64_t>(1, std::min(2 * a->num_sms / blocks, std::min<int64_t>(tiles / 4, 64)));
+        p.splits = (int)std::max<int64_t>(1, std::min(a->num_sms / blocks, std::min<int64_t>(tiles / 4, 64)));
     return p;
 }
 
@@ -527,7 +545,7 @@ pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, 
         kern<<<dim3(plan.blocks, plan.rows, (unsigned)plan.splits), kAttnThreads, S::kSmem, st>>>(mq, mk, mv, P);
         if (plan.splits > 1) {
             if (cudaGetLastError() != cudaSuccess) return PE_ERR_CUDA;
-            pe_attn_join_kernel<<<(unsigned)(((int64_t)a->Hq * Nq + 7) / 8), 256, 0, st>>>(P);
+            return finish(launch_after(pe_attn_join_kernel, dim3((unsigned)(((int64_t)a->Hq * Nq + 7) / 8)), 256, 0, st, P));
         }
         return finish(cudaGetLastError());
     });
@@ -581,17 +599,19 @@ pe_status pe_attention_backward(pe_attention *a, int n_seq, const int32_t *cu_q,
         auto dq_kern = pe_attn_bwd_kernel<DP, false>;
         auto dkv_kern = pe_attn_bwd_kernel<DP, true>;
         static std::atomic<uint64_t> dq_done{0}, dkv_done{0};
-        if (!ready_to_launch(dq_kern, kBwdSmem<DP>, a->dev, dq_done) ||
-            !ready_to_launch(dkv_kern, kBwdSmem<DP>, a->dev, dkv_done))
+        if (!ready_to_launch(dq_kern, BwdShape<DP, false>::kSmem, a->dev, dq_done) ||
+            !ready_to_launch(dkv_kern, BwdShape<DP, true>::kSmem, a->dev, dkv_done))
             return PE_ERR_CUDA;
         if (Nq > 0) {
             const dim3 grid(max_tiles(Nq, n_seq, kTile), (unsigned)a->Hq);
-            dq_kern<<<grid, kAttnThreads, kBwdSmem<DP>, st>>>(mq, md, mk, mv, P);
+            dq_kern<<<grid, kAttnThreads, BwdShape<DP, false>::kSmem, st>>>(mq, md, mk, mv, P);
             if (cudaGetLastError() != cudaSuccess) return PE_ERR_CUDA;
         }
         if (Nk > 0) {
             const dim3 grid(max_tiles(Nk, n_seq, kTile), (unsigned)a->Hkv);
-            dkv_kern<<<grid, kAttnThreads, kBwdSmem<DP>, st>>>(mk, mv, mq, md, P);
+            const size_t smem = BwdShape<DP, true>::kSmem;
+            if (Nq > 0) return finish(launch_after(dkv_kern, grid, kAttnThreads, smem, st, mk, mv, mq, md, P));
+            dkv_kern<<<grid, kAttnThreads, smem, st>>>(mk, mv, mq, md, P);
         }
         return finish(cudaGetLastError());
     });
