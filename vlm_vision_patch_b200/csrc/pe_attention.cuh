@@ -311,7 +311,7 @@ __host__ __device__ constexpr uint32_t idesc_b_mn(int M, int N) { return idesc_b
 // key head stand side by side in one tile, so its keys are read once for all of
 // them, and several blocks divide the key axis; a second kernel joins their parts.
 
-constexpr int kAttnThreads = 384;             // 168 registers each = 256 * 224 + 128 * 56
+constexpr int kAttnThreads = 384;             // 168 registers each = 256 * 208 + 128 * 88
 constexpr int kPolyOf4 = 1;                     // of four pairs of exponentials, how many the FMA pipes take
 
 template <int DP>
@@ -718,10 +718,10 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     const int kb = from * KT, n_max = to - from;
     const int n0 = min(max(all0 - from, 0), n_max), n1 = min(max(all1 - from, 0), n_max);
     if (warp < 8) {
-        regs_up<224>();
+        regs_up<208>();
         if (warp < 4 || two) fwd_softmax<DP>(P, B, w, warp >> 2, warp < 4 ? n0 : n1, warp < 4 ? n1 : n0, kb, h);
     } else {
-        regs_down<56>();
+        regs_down<88>();
         if (warp == 8) fwd_load<DP>(P, B, w, mq, mk, mv, sq, ring, two, n_max, kb, h, hk);
         else if (warp < (two ? 11 : 10)) fwd_mma<DP>(B, w, sq, ring, warp - 9, warp == 9 ? n0 : n1, n_max, kb);
     }
@@ -774,6 +774,8 @@ struct BwdShape {
     static constexpr uint32_t kStage = 2 * kOne + (KEYS ? kStats : 0);
     static constexpr int kFit = (212 * 1024 - kFixed) / kStage, kStages = kFit < 8 ? kFit : 8;
     static constexpr uint32_t kTiles = 2 * kKept + kStages * 2 * kOne;
+    // a warp that issues every second tile's scores meets every phase of its slots only then
+    static_assert(kStages >= 2 && kStages % 2 == 0, "ring depth");
     static constexpr size_t kSmem = kFixed + (size_t)kStages * kStage;
 };
 constexpr int kBwdMaxStages = 8;
@@ -835,6 +837,26 @@ struct BwdCols {
     __device__ static uint32_t ds(int b) { return kAlias ? b * kBuf + 64 : (kShared ? kDs : kDs + 32 * b); }
 };
 
+// p and ds of 16 columns, the first of them `col`, as bf16 pairs.  CUT: some are masked.
+template <bool KEYS, bool CUT>
+__device__ __forceinline__ void bwd_chunk(const uint32_t (&s)[16], const uint32_t (&d)[16], float2 sl2, float nlse2,
+                                          float ndelta, int col, int from, int upto, uint32_t (&pp)[8], uint32_t (&pd)[8]) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+        const float2 sc = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+        const float2 dp = make_float2(__uint_as_float(d[e]), __uint_as_float(d[e + 1]));
+        const float2 x = KEYS ? mul2(sc, sl2) : fma2(sc, sl2, both(nlse2));
+        float2 p = make_float2(ex2(x.x), ex2(x.y));
+        float2 q = mul2(p, KEYS ? dp : add2(dp, both(ndelta)));
+        if (CUT) {
+            if (KEYS ? col + e < from : col + e >= upto) p.x = q.x = 0.f;
+            if (KEYS ? col + e + 1 < from : col + e + 1 >= upto) p.y = q.y = 0.f;
+        }
+        if (KEYS) pp[e / 2] = pack_bf16x2(p.x, p.y);
+        pd[e / 2] = pack_bf16x2(q.x, q.y);
+    }
+}
+
 // p and ds of every second streamed tile, then half of the results; the 128
 // threads of group g, one kept row each.
 template <int DP, bool KEYS>
@@ -893,27 +915,24 @@ __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const
         }
         // queries a key row sees start at i - shift; keys a query row sees end at limit
         const bool cut = __any_sync(0xffffffffu, KEYS ? P.causal && y < i - shift : y + kStream > limit);
+        // the columns that count: from `from` on (keys), before `limit` (queries)
+        const int from = i - shift - y, upto = limit - y;
         uint32_t pp[4][8], pd[4][8];
+        if (cut) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c)
+                bwd_chunk<KEYS, true>(s[c], d[c], sl2, nlse2, ndelta, 16 * c, from, upto, pp[c], pd[c]);
+        } else {
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-                const float2 sc = make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
-                const float2 dp = make_float2(__uint_as_float(d[c][e]), __uint_as_float(d[c][e + 1]));
-                const float2 x = KEYS ? mul2(sc, sl2) : fma2(sc, sl2, both(nlse2));
-                float2 p = make_float2(ex2(x.x), ex2(x.y));
-                float2 q = mul2(p, KEYS ? dp : add2(dp, both(ndelta)));
-                if (cut) {
-                    const int col = y + 16 * c + e;
-                    if (KEYS ? col < i - shift : col >= limit) p.x = q.x = 0.f;
-                    if (KEYS ? col + 1 < i - shift : col + 1 >= limit) p.y = q.y = 0.f;
-                }
-                if (KEYS) pp[c][e / 2] = pack_bf16x2(p.x, p.y);
-                pd[c][e / 2] = pack_bf16x2(q.x, q.y);
-            }
-        // the sums have read what was in its place
+            for (int c = 0; c < 4; ++c)
+                bwd_chunk<KEYS, false>(s[c], d[c], sl2, nlse2, ndelta, 16 * c, from, upto, pp[c], pd[c]);
+        }
+        // The sums have read what was in its place: the tile before (of the other group)
+        // when the place is shared, this group's last tile otherwise.  A barrier per
+        // group, since a wait by parity may only look for the phase after the last one
+        // known to be over; that is so here, as tile j - 3 was waited for at j - 2.
         if (T::kShared ? j > 0 : !T::kAlias && n > 0) {
-            if (!warp_wait(&B.acc_done[T::kShared ? 0 : g], ((T::kShared ? j : n) - 1) & 1, abort)) return;
+            if (!warp_wait(&B.acc_done[T::kShared ? 1 - g : g], (T::kShared ? (j - 1) >> 1 : n - 1) & 1, abort)) return;
             tc_fence_after();
         }
 #pragma unroll
@@ -1093,7 +1112,7 @@ __device__ __forceinline__ void bwd_sums(BwdBars &B, const Stream &st, uint8_t *
         if (one) {
             if (KEYS) add(tm + T::kAcc0, tm + T::p(b), z1, steps, j > 0);
             add(tm + T::kAcc1, tm + T::ds(b), z0, steps, j > 0);
-            mma_commit(T::kAlias ? &B.s_free[b] : &B.acc_done[T::kShared ? 0 : b]);
+            mma_commit(T::kAlias ? &B.s_free[b] : &B.acc_done[b]);
             mma_commit(&B.empty[slot]);
             if (j + 1 == st.n) mma_commit(&B.acc_full);
         }
@@ -1169,10 +1188,10 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
     }
     const Stream st = stream_of<KEYS>(P, w);
     if (warp < 8) {
-        regs_up<224>();
+        regs_up<208>();
         bwd_group<DP, KEYS>(P, B, w, st, warp >> 2, h);
     } else {
-        regs_down<56>();
+        regs_down<88>();
         if (st.n > 0) {
             if (warp == 8) bwd_load<DP, KEYS>(P, B, w, st, mx0, mx1, my0, my1, kept, ring, stats, h);
             else if (warp < 11) bwd_scores<DP, KEYS>(B, st, kept, ring, select, stats, warp - 9);

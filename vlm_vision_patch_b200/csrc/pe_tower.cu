@@ -203,7 +203,7 @@ bool ready_to_launch(Kernel kern, size_t smem, int dev, std::atomic<uint64_t> &d
     if (done.load(std::memory_order_relaxed) & bit) return true;
     cudaFuncAttributes at;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
-        cudaFuncGetAttributes(&at, kern) != cudaSuccess || at.numRegs * kAttnThreads < 256 * 224 + 128 * 56)
+        cudaFuncGetAttributes(&at, kern) != cudaSuccess || at.numRegs * kAttnThreads < 256 * 208 + 128 * 88)
         return false;
     done.fetch_or(bit, std::memory_order_relaxed);
     return true;
