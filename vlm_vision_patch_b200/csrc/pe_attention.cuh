@@ -188,8 +188,9 @@ struct AttnParams {
     HeadsPtr q, k, v, out, dout, dq, dk, dv;
     float *lse;                   // [Hq, Nq]
     int pack;                     // query heads of a key head side by side in a tile's rows (forward; 1: none)
-    int splits;                   // parts of the key axis, a block each (forward)
-    float *part_out, *part_lse2;  // [splits, Hq, Nq, D] and [splits, Hq, Nq] (base 2), when splits > 1
+    int splits;                   // parts, a block each: of the key axis (forward), of the heads that share a key head (keys)
+    float *part_out, *part_lse2;  // when splits > 1: forward [splits, Hq, Nq, D] and [splits, Hq, Nq] (base 2);
+                                  // keys [splits, 2, Nk, Hkv, D], dv then dk
     uint4 *stat;                  // [Hq, Nq]: -lse / scale and -dout . out, three bf16 and a 0 each (backward)
     int *err;
 };
@@ -206,7 +207,8 @@ constexpr int kTile = 128;                  // rows of a tile: queries or keys
 constexpr int kChunkBytes = kTile * 128;    // 128 rows of 64 bf16, 128-byte swizzle
 constexpr float kLog2e = 1.4426950408889634f;
 
-// The tile of sequence rows that a block works on.
+// The tile of sequence rows that a block works on.  (Under a causal mask the blocks
+// with the most to do come first: the last query rows, the first key rows.)
 struct Work {
     int q0, lq, k0, lk;    // the sequence's rows; lq, lk >= 0
     int row;               // first row of the tile within the sequence, or -1: nothing to do
@@ -486,6 +488,16 @@ __device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, con
     else if (P.lse) P.lse[at] = limit > 0 ? m * P.scale + logf(l) : -INFINITY;
 }
 
+// Whether row r belongs to a sequence of `cu`.
+__device__ __forceinline__ bool in_sequence(const int32_t *cu, int n_seq, int n, int r) {
+    int lo = -1, hi = n_seq - 1;                          // the last sequence that begins at or before r
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (boundary(cu, mid, n) <= r) lo = mid; else hi = mid - 1;
+    }
+    return lo >= 0 && r < boundary(cu, lo + 1, n);
+}
+
 // Joins the parts of a row and head (one warp each): out = sum_z w_z out_z / sum_z
 // w_z with w_z = 2^(lse2_z - max).
 __global__ void __launch_bounds__(256) pe_attn_join_kernel(const __grid_constant__ AttnParams P) {
@@ -494,12 +506,7 @@ __global__ void __launch_bounds__(256) pe_attn_join_kernel(const __grid_constant
     const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);          // [Hq, Nq]
     if (at >= (int64_t)P.Hq * P.Nq) return;
     const int h = (int)(at / P.Nq), r = (int)(at - (int64_t)h * P.Nq);
-    int lo = -1, hi = P.n_seq - 1;                        // the last sequence that begins at or before r
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (boundary(P.cu_q, mid, P.Nq) <= r) lo = mid; else hi = mid - 1;
-    }
-    if (lo < 0 || r >= boundary(P.cu_q, lo + 1, P.Nq)) return;                // a row of no sequence
+    if (!in_sequence(P.cu_q, P.n_seq, P.Nq, r)) return;
     const int64_t step = (int64_t)P.Hq * P.Nq;
     // at most 64 parts: a lane holds two of their statistics
     const float l0 = lane < P.splits ? P.part_lse2[lane * step + at] : -INFINITY;
@@ -671,7 +678,7 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.y, hk = P.pack > 1 ? h : h / (P.Hq / P.Hkv), rows = kTile / P.pack;
     if (warp == 9) {
-        const Work w = find_work(P, false, blockIdx.x, 2 * rows);
+        const Work w = find_work(P, false, P.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x, 2 * rows);
         if (lane == 0) {
             B.w = w;
             B.abort = 0;
@@ -804,16 +811,19 @@ __device__ __forceinline__ uint2 split3(float v) {
 // shares the key head, from the first that sees the tile's first key.
 struct Stream {
     int first, per_head, n;                       // first tile, tiles per head, tiles in all
+    int head;                                     // first query head (keys)
 };
 
 template <bool KEYS>
-__device__ __forceinline__ Stream stream_of(const AttnParams &P, const Work &w) {
-    Stream st = {0, 0, 0};
+__device__ __forceinline__ Stream stream_of(const AttnParams &P, const Work &w, int h) {
+    Stream st = {0, 0, 0, 0};
     if (KEYS) {
+        const int share = P.Hq / P.Hkv, from = share * blockIdx.z / P.splits, to = share * (blockIdx.z + 1) / P.splits;
+        st.head = h * share + from;
         const int i0 = P.causal ? max(0, w.row - (w.lk - w.lq)) : 0;
         st.first = i0 / kStream;
         st.per_head = max((w.lq + kStream - 1) / kStream - st.first, 0);
-        st.n = st.per_head * (P.Hq / P.Hkv);
+        st.n = st.per_head * (to - from);
     } else {
         const int last = min(w.row + kTile, w.lq) - 1;
         st.per_head = st.n = (keys_seen(P, w, last) + kStream - 1) / kStream;
@@ -962,13 +972,22 @@ __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const
             tmem_ld_x16(acc + 16 * c, o[0]);
             tmem_ld_wait_for(o);
         }
+        if (!mine) continue;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            uint32_t pk[4];
+            if (16 * c + 8 * q >= P.D) continue;
+            float v[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                pk[e] = pack_bf16x2(__uint_as_float(o[0][8 * q + 2 * e]) * f, __uint_as_float(o[0][8 * q + 2 * e + 1]) * f);
-            if (mine && 16 * c + 8 * q < P.D) st_global_v4(out + 16 * c + 8 * q, pk[0], pk[1], pk[2], pk[3]);
+            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[0][8 * q + e]) * f;
+            if (KEYS && P.splits > 1) {
+                float4 *dst = reinterpret_cast<float4 *>(
+                    P.part_out + ((((int64_t)blockIdx.z * 2 + g) * P.Nk + w.k0 + i) * P.Hkv + h) * P.D + 16 * c + 8 * q);
+                dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+                st_global_v4(out + 16 * c + 8 * q, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+            }
         }
     }
 }
@@ -982,7 +1001,7 @@ __device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const 
     constexpr int kC = kChunks<DP>;
     constexpr uint32_t kKept = S::kKept, kOne = S::kOne;                       // bytes of one kept / streamed tile
     volatile int *abort = &B.abort;
-    const int lane = threadIdx.x & 31, share = P.Hq / P.Hkv;
+    const int lane = threadIdx.x & 31;
     const int y_len = KEYS ? w.lq : w.lk;                   // streamed rows of the sequence
     const int x_row = (KEYS ? w.k0 : w.q0) + w.row;
     if (lane == 0) {
@@ -993,7 +1012,7 @@ __device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const 
                     tma_load_3d(smem_addr(kept + t * kKept + c * kChunkBytes + half * kStreamChunk), t ? &mx1 : &mx0,
                                 smem_addr(&B.xfull), 64 * c, h, x_row + half * kStream);
     }
-    int f = 0, tails = 0, tile = 0, y_head = KEYS ? h * share : h / share;
+    int f = 0, tails = 0, tile = 0, y_head = KEYS ? st.head : h / (P.Hq / P.Hkv);
     bool ok = true;
     Slot<S::kStages> r;
     for (; f < st.n; ++f, ++tile, r.next()) {
@@ -1135,7 +1154,7 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.y;
     if (warp == 9) {
-        const Work w = find_work(P, KEYS, blockIdx.x, kTile);
+        const Work w = find_work(P, KEYS, P.causal && !KEYS ? gridDim.x - 1 - blockIdx.x : blockIdx.x, kTile);
         if (lane == 0) {
             B.w = w;
             B.abort = 0;
@@ -1181,12 +1200,13 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
     const Work w = B.w;
     // the key kernel starts as the query kernel, whose statistics it reads, ends
     if (!KEYS) griddep_launch_dependents();
+    if (KEYS && P.splits > 1) griddep_launch_dependents();  // the joining kernel
     if (KEYS && warp == 8) griddep_wait();
     if (w.row < 0) {                                        // more blocks than tiles
         if (warp == 8) tmem_dealloc(B.tmem, 512);
         return;
     }
-    const Stream st = stream_of<KEYS>(P, w);
+    const Stream st = stream_of<KEYS>(P, w, h);
     if (warp < 8) {
         regs_up<208>();
         bwd_group<DP, KEYS>(P, B, w, st, warp >> 2, h);
@@ -1206,6 +1226,28 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
         tc_fence_after();
         tmem_dealloc(B.tmem, 512);
     }
+}
+
+// Adds the parts of dk and dv in order (one warp per key row and key head).
+__global__ void __launch_bounds__(256) pe_attn_join_grads_kernel(const __grid_constant__ AttnParams P) {
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);          // [Nk, Hkv]
+    if (at >= (int64_t)P.Nk * P.Hkv || 4 * lane >= P.D) return;
+    const int r = (int)(at / P.Hkv), h = (int)(at - (int64_t)r * P.Hkv);
+    if (!in_sequence(P.cu_k, P.n_seq, P.Nk, r)) return;
+    const int64_t step = (int64_t)P.Nk * P.Hkv * P.D;
+    const float *src = P.part_out + at * P.D + 4 * lane;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f), k = v;
+#pragma unroll 4
+    for (int z = 0; z < P.splits; ++z) {
+        const float4 a = *reinterpret_cast<const float4 *>(src + 2 * z * step);
+        const float4 b = *reinterpret_cast<const float4 *>(src + (2 * z + 1) * step);
+        v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+        k.x += b.x, k.y += b.y, k.z += b.z, k.w += b.w;
+    }
+    *reinterpret_cast<uint2 *>(P.dv.at(r, h) + 4 * lane) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    *reinterpret_cast<uint2 *>(P.dk.at(r, h) + 4 * lane) = make_uint2(pack_bf16x2(k.x, k.y), pack_bf16x2(k.z, k.w));
 }
 
 }  // namespace pe

@@ -260,6 +260,16 @@ FwdPlan plan_forward(const pe_attention *a, int n_seq, int64_t Nq, int64_t Nk) {
     return p;
 }
 
+// Parts of the heads that share a key head, a block each, of the key kernel: when
+// its blocks are fewer than two a SM, as long ones (the first keys of a causal
+// sequence) would be all that runs in the end.
+int plan_key_parts(const pe_attention *a, int n_seq, int64_t Nq, int64_t Nk) {
+    if (n_seq == 0 || Nq == 0 || Nk == 0) return 1;
+    const int64_t blocks = std::max<int64_t>((Nk + kTile - 1) / kTile, std::min<int64_t>(n_seq, Nk)) * a->Hkv;
+    const int64_t want = (2 * (int64_t)a->num_sms + blocks - 1) / blocks;
+    return (int)std::min<int64_t>(a->Hq / a->Hkv, want);
+}
+
 }  // namespace
 
 extern "C" {
@@ -476,7 +486,11 @@ pe_status pe_attention_last_error(pe_attention *a) {
 
 int64_t pe_attention_workspace(const pe_attention *a, int n_seq, int64_t Nq, int64_t Nk, int backward) {
     if (check_attention(a, n_seq, Nq, Nk) != PE_OK || (backward != 0 && backward != 1)) return -1;
-    if (backward) return (int64_t)a->Hq * Nq * (int64_t)sizeof(uint4);
+    if (backward) {
+        const int parts = plan_key_parts(a, n_seq, Nq, Nk);
+        return (int64_t)a->Hq * Nq * (int64_t)sizeof(uint4) +
+               (parts > 1 ? (int64_t)parts * 2 * Nk * a->Hkv * a->D * (int64_t)sizeof(float) : 0);
+    }
     if (n_seq == 0 || Nq == 0) return 0;
     const int splits = plan_forward(a, n_seq, Nq, Nk).splits;
     return splits > 1 ? (int64_t)splits * a->Hq * Nq * (a->D + 1) * (int64_t)sizeof(float) : 0;
@@ -585,6 +599,8 @@ pe_status pe_attention_backward(pe_attention *a, int n_seq, const int32_t *cu_q,
     P.dv = heads_ptr(dv, Nk, a->Hkv);
     P.lse = const_cast<float *>(lse);
     P.stat = static_cast<uint4 *>(ws);
+    P.splits = plan_key_parts(a, n_seq, Nq, Nk);
+    P.part_out = reinterpret_cast<float *>(P.stat + (int64_t)a->Hq * Nq);
     cudaStream_t st = (cudaStream_t)stream;
     CUtensorMap mq, mk, mv, md;
     if (Nq > 0 && (!make_heads_tmap(&mq, q, Nq, a->Hq, D, kStream) || !make_heads_tmap(&md, dout, Nq, a->Hq, D, kStream)))
@@ -608,10 +624,15 @@ pe_status pe_attention_backward(pe_attention *a, int n_seq, const int32_t *cu_q,
             if (cudaGetLastError() != cudaSuccess) return PE_ERR_CUDA;
         }
         if (Nk > 0) {
-            const dim3 grid(max_tiles(Nk, n_seq, kTile), (unsigned)a->Hkv);
+            const dim3 grid(max_tiles(Nk, n_seq, kTile), (unsigned)a->Hkv, (unsigned)P.splits);
             const size_t smem = BwdShape<DP, true>::kSmem;
-            if (Nq > 0) return finish(launch_after(dkv_kern, grid, kAttnThreads, smem, st, mk, mv, mq, md, P));
-            dkv_kern<<<grid, kAttnThreads, smem, st>>>(mk, mv, mq, md, P);
+            if (Nq == 0) {
+                dkv_kern<<<grid, kAttnThreads, smem, st>>>(mk, mv, mq, md, P);
+                return finish(cudaGetLastError());
+            }
+            if (launch_after(dkv_kern, grid, kAttnThreads, smem, st, mk, mv, mq, md, P) != cudaSuccess) return PE_ERR_CUDA;
+            if (P.splits > 1)
+                return finish(launch_after(pe_attn_join_grads_kernel, dim3((unsigned)((Nk * a->Hkv + 7) / 8)), 256, 0, st, P));
         }
         return finish(cudaGetLastError());
     });
