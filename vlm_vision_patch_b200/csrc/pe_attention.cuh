@@ -187,6 +187,7 @@ struct AttnParams {
     float scale;
     HeadsPtr q, k, v, out, dout, dq, dk, dv;
     float *lse;                   // [Hq, Nq]
+    int tiles;                    // query tiles of a block, 1 or 2 (forward)
     int pack;                     // query heads of a key head side by side in a tile's rows (forward; 1: none)
     int splits;                   // parts, a block each: of the key axis (forward), of the heads that share a key head (keys)
     float *part_out, *part_lse2;  // when splits > 1: forward [splits, Hq, Nq, D] and [splits, Hq, Nq] (base 2);
@@ -299,8 +300,8 @@ __host__ __device__ constexpr uint32_t idesc_b_mn(int M, int N) { return idesc_b
 
 // ------------------------------------------------------------- forward
 //
-// A block takes 256 query rows of one sequence and head as two tiles of 128,
-// and streams the sequence's keys and values past them.  Roles: warps 0-3 and
+// A block takes 256 query rows of one sequence and head as two tiles of 128 (one
+// tile when there are blocks for half of the SMs at most), and streams the sequence's keys and values past them.  Roles: warps 0-3 and
 // 4-7 do the softmax of tile 0 and 1 (one thread per row: row maximum and sum
 // need no shuffles), warp 8 loads, warp 9 issues the MMAs.  Scores (fp32) and
 // probabilities (bf16) have columns of their own in tensor memory, so the scores
@@ -678,11 +679,11 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.y, hk = P.pack > 1 ? h : h / (P.Hq / P.Hkv), rows = kTile / P.pack;
     if (warp == 9) {
-        const Work w = find_work(P, false, P.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x, 2 * rows);
+        const Work w = find_work(P, false, P.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x, P.tiles * rows);
         if (lane == 0) {
             B.w = w;
             B.abort = 0;
-            const int tiles = w.lq - w.row > rows ? 2 : 1;  // each gives a slot back
+            const int tiles = P.tiles > 1 && w.lq - w.row > rows ? 2 : 1;  // each gives a slot back
             for (int i = 0; i < S::kStages; ++i) mbar_init(smem_addr(&B.full[i]), 1), mbar_init(smem_addr(&B.empty[i]), tiles);
             mbar_init(smem_addr(&B.tail), 1);
             mbar_init(smem_addr(&B.qfull), 1);
@@ -716,9 +717,9 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     // key tiles that each query tile meets (the second tile may be missing) ...
     auto tiles_of = [&](int t) {
         const int last = min(w.row + (t + 1) * rows, w.lq) - 1;
-        return w.lq - w.row > t * rows ? (keys_seen(P, w, last) + KT - 1) / KT : 0;
+        return t < P.tiles && w.lq - w.row > t * rows ? (keys_seen(P, w, last) + KT - 1) / KT : 0;
     };
-    const bool two = w.lq - w.row > rows;
+    const bool two = P.tiles > 1 && w.lq - w.row > rows;
     const int all0 = tiles_of(0), all1 = tiles_of(1), all = max(all0, all1);
     // ... and this block's part of them, from key kb on
     const int from = (int)((int64_t)all * blockIdx.z / P.splits), to = (int)((int64_t)all * (blockIdx.z + 1) / P.splits);

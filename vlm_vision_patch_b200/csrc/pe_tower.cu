@@ -238,7 +238,7 @@ pe_status check_attention(const pe_attention *a, int n_seq, int64_t Nq, int64_t 
 
 // How a forward call lays its rows and keys out over blocks, from the sizes alone.
 struct FwdPlan {
-    int pack, splits;
+    int tiles, pack, splits;
     unsigned blocks, rows;       // blocks of one head and split; heads or, packed, key heads
 };
 
@@ -247,12 +247,15 @@ FwdPlan plan_forward(const pe_attention *a, int n_seq, int64_t Nq, int64_t Nk) {
     FwdPlan p;
     // an average sequence's rows of all heads that share a key head fit one tile
     p.pack = share > 1 && share <= kTile && Nq * share <= (int64_t)kTile * n_seq ? share : 1;
-    p.blocks = max_tiles(Nq, n_seq, 2 * (kTile / p.pack));
     p.rows = (unsigned)(p.pack > 1 ? a->Hkv : a->Hq);
+    // at least so many blocks of two tiles; one tile a block ends sooner while SMs are idle
+    const int rows = kTile / p.pack;
+    auto at_least = [&](int r) { return std::max<int64_t>((Nq + r - 1) / r, std::min<int64_t>(n_seq, Nq)) * p.rows; };
+    p.tiles = at_least(2 * rows) * 2 <= a->num_sms ? 1 : 2;
+    const int64_t blocks = at_least(p.tiles * rows);
+    p.blocks = max_tiles(Nq, n_seq, p.tiles * rows);
     // With blocks for less than a quarter of the SMs the key axis is divided until there
     // is one a SM, but into no less than 4 tiles of an average sequence.
-    const int rows = 2 * (kTile / p.pack);
-    const int64_t blocks = std::max<int64_t>((Nq + rows - 1) / rows, std::min<int64_t>(n_seq, Nq)) * p.rows;
     const int64_t tiles = Nk / n_seq / 128;
     p.splits = 1;
     if (blocks * 4 <= a->num_sms)
@@ -536,6 +539,7 @@ pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, 
     P.v = heads_ptr(v, Nk, a->Hkv);
     P.lse = lse;
     const FwdPlan plan = plan_forward(a, n_seq, Nq, Nk);
+    P.tiles = plan.tiles;
     P.pack = plan.pack;
     P.splits = plan.splits;
     if (plan.splits > 1) {
