@@ -789,7 +789,8 @@ struct BwdShape {
 constexpr int kBwdMaxStages = 8;
 
 struct BwdBars {
-    uint64_t full[kBwdMaxStages], empty[kBwdMaxStages], tail, xfull, s_full[2], s_free[2], d_full[2], acc_done[2], acc_full, drain[3];
+    uint64_t full[kBwdMaxStages], empty[kBwdMaxStages], tail, xfull, s_full[2], s_free[2], d_full[2], acc_done[2], acc_full, off_full, drain[3];
+    float off[2][kTile];                          // what delta is off by, each group's part
     uint32_t tmem;
     int abort;
     Work w;
@@ -813,11 +814,18 @@ __device__ __forceinline__ uint2 split3(float v) {
 struct Stream {
     int first, per_head, n;                       // first tile, tiles per head, tiles in all
     int head;                                     // first query head (keys)
+    int total;                                    // tiles streamed: n, or twice that (short query rows)
 };
+
+// delta comes from the stored output, whose rounding is as large as ds itself where
+// a row sees few keys.  Rows of at most this many key tiles are swept twice: the
+// first time only sums ds, which is what delta is off by.  (Beyond 256 keys it
+// moves dq's error by 1 part in 100 and would cost a third of the kernel.)
+constexpr int kSweepTwice = 4;
 
 template <bool KEYS>
 __device__ __forceinline__ Stream stream_of(const AttnParams &P, const Work &w, int h) {
-    Stream st = {0, 0, 0, 0};
+    Stream st = {0, 0, 0, 0, 0};
     if (KEYS) {
         const int share = P.Hq / P.Hkv, from = share * blockIdx.z / P.splits, to = share * (blockIdx.z + 1) / P.splits;
         st.head = h * share + from;
@@ -829,6 +837,7 @@ __device__ __forceinline__ Stream stream_of(const AttnParams &P, const Work &w, 
         const int last = min(w.row + kTile, w.lq) - 1;
         st.per_head = st.n = (keys_seen(P, w, last) + kStream - 1) / kStream;
     }
+    st.total = !KEYS && st.n <= kSweepTwice ? 2 * st.n : st.n;
     return st;
 }
 
@@ -895,23 +904,20 @@ __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const
                     ndelta -= bf16lo_to_f32(x[k]) * bf16lo_to_f32(y[k]) + bf16hi_to_f32(x[k]) * bf16hi_to_f32(y[k]);
             }
             nlse2 = -P.lse[at] * kLog2e;
-            if (g == 0) {
-                // a row that sees no key has lse = -inf; with a large finite value its p is 0 and no product inf * 0
-                const uint2 u = split3(limit > 0 ? -P.lse[at] / P.scale : -1e30f), v = split3(ndelta);
-                P.stat[at] = make_uint4(u.x, u.y, v.x, v.y);
-            }
         }
     }
-    const int shift = w.lk - w.lq;
-    int tile = g;                                           // of the current head's streamed tiles
-    for (int j = g; j < st.n; j += 2, tile += 2) {
-        const int n = j >> 1;
-        if (KEYS)
-            while (tile >= st.per_head) tile -= st.per_head;
-        if (!warp_wait(&B.s_full[g], n & 1, abort)) return;
+    // the row's statistics for the key kernel
+    auto put_stat = [&] {
+        if (KEYS || !mine || g != 0) return;
+        // a row that sees no key has lse = -inf; with a large finite value its p is 0 and no product inf * 0
+        const int64_t at = (int64_t)h * P.Nq + w.q0 + i;
+        const uint2 u = split3(limit > 0 ? -P.lse[at] / P.scale : -1e30f), v = split3(ndelta);
+        P.stat[at] = make_uint4(u.x, u.y, v.x, v.y);
+    };
+    // scores and dp of tile j, the n-th of this buffer, into registers
+    auto take = [&](int n, uint32_t (&s)[4][16], uint32_t (&d)[4][16]) {
+        if (!warp_wait(&B.s_full[g], n & 1, abort)) return false;
         tc_fence_after();
-        const int y = (st.first + tile) * kStream;          // first streamed row
-        uint32_t s[4][16], d[4][16];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             tmem_ld_x16(ts + 16 * c, s[c]);
@@ -924,6 +930,40 @@ __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&B.s_free[g]));
         }
+        return true;
+    };
+    int tile = g, j = g;                                    // of the current head's streamed tiles; of all
+    if (!KEYS && st.total > st.n) {                         // the first of two sweeps
+        float off = 0.f;
+        for (; j < st.n; j += 2, tile += 2) {
+            uint32_t s[4][16], d[4][16];
+            if (!take(j >> 1, s, d)) return;
+            const int upto = limit - tile * kStream;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float p = ex2(fmaf(__uint_as_float(s[c][e]), sl2.x, nlse2));
+                    if (16 * c + e < upto) off = fmaf(p, __uint_as_float(d[c][e]) + ndelta, off);
+                }
+            if (j > g && !warp_wait(&B.acc_done[g], ((j >> 1) - 1) & 1, abort)) return;   // every phase is met
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&B.d_full[g]));
+        }
+        B.off[g][(warp & 3) * 32 + lane] = off;             // both groups meet
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&B.off_full));
+        if (!warp_wait(&B.off_full, 0, abort)) return;
+        ndelta -= B.off[0][(warp & 3) * 32 + lane] + B.off[1][(warp & 3) * 32 + lane];
+    }
+    put_stat();
+    const int shift = w.lk - w.lq;
+    for (; j < st.total; j += 2, tile += 2) {
+        const int n = j >> 1;
+        while (tile >= st.per_head) tile -= st.per_head;
+        uint32_t s[4][16], d[4][16];
+        if (!take(n, s, d)) return;
+        const int y = (st.first + tile) * kStream;          // first streamed row
         // queries a key row sees start at i - shift; keys a query row sees end at limit
         const bool cut = __any_sync(0xffffffffu, KEYS ? P.causal && y < i - shift : y + kStream > limit);
         // the columns that count: from `from` on (keys), before `limit` (queries)
@@ -1016,11 +1056,14 @@ __device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const 
     int f = 0, tails = 0, tile = 0, y_head = KEYS ? st.head : h / (P.Hq / P.Hkv);
     bool ok = true;
     Slot<S::kStages> r;
-    for (; f < st.n; ++f, ++tile, r.next()) {
+    for (; f < st.total; ++f, ++tile, r.next()) {
         const int slot = r.at;
         ok = warp_wait(&B.empty[slot], r.phase ^ 1, abort);
         if (!ok) break;
-        if (KEYS && tile == st.per_head) tile = 0, ++y_head;
+        if (tile == st.per_head) {                          // the next head, or the second sweep
+            tile = 0;
+            if (KEYS) ++y_head;
+        }
         const int row = (st.first + tile) * kStream;
         const int y_row = (KEYS ? w.q0 : w.k0) + row;
         const int valid = min(y_len - row, kStream);
@@ -1074,7 +1117,7 @@ __device__ __forceinline__ void bwd_scores(BwdBars &B, const Stream &st, uint8_t
     bool ok = warp_wait(&B.xfull, 0, abort);
     Slot<S::kStages> r;
     r.at = b;
-    for (int j = b; j < st.n && ok; j += 2, r.next(2)) {
+    for (int j = b; j < st.total && ok; j += 2, r.next(2)) {
         const int n = j >> 1, slot = r.at;
         ok = warp_wait(&B.full[slot], r.phase, abort) && (n == 0 || warp_wait(&B.s_free[b], (n - 1) & 1, abort));
         if (!ok) break;
@@ -1121,20 +1164,24 @@ __device__ __forceinline__ void bwd_sums(BwdBars &B, const Stream &st, uint8_t *
     bool ok = true;
     Slot<S::kStages> r;
     int tile = 0;
-    for (int j = 0; j < st.n && ok; ++j, ++tile, r.next()) {
-        if (KEYS && tile == st.per_head) tile = 0;
+    const int second = st.total - st.n;
+    for (int j = 0; j < st.total && ok; ++j, ++tile, r.next()) {
+        if (tile == st.per_head) tile = 0;
         const int b = j & 1, slot = r.at, row = (st.first + tile) * kStream;
         const int steps = (min(y_len - row, kStream) + 15) / 16;
         ok = warp_wait(&B.full[slot], r.phase, abort) && warp_wait(&B.d_full[b], (j >> 1) & 1, abort);
         if (!ok) break;
         tc_fence_after();
         const uint32_t z0 = desc_mn<kStreamChunk>(smem_addr(ring + slot * 2 * kOne)), z1 = z0 + (kOne >> 4);
-        if (one) {
-            if (KEYS) add(tm + T::kAcc0, tm + T::p(b), z1, steps, j > 0);
-            add(tm + T::kAcc1, tm + T::ds(b), z0, steps, j > 0);
+        if (one && j < second) {                            // the first of two sweeps adds nothing
+            mbar_arrive(smem_addr(&B.acc_done[b]));
+            mbar_arrive(smem_addr(&B.empty[slot]));
+        } else if (one) {
+            if (KEYS) add(tm + T::kAcc0, tm + T::p(b), z1, steps, j > second);
+            add(tm + T::kAcc1, tm + T::ds(b), z0, steps, j > second);
             mma_commit(T::kAlias ? &B.s_free[b] : &B.acc_done[b]);
             mma_commit(&B.empty[slot]);
-            if (j + 1 == st.n) mma_commit(&B.acc_full);
+            if (j + 1 == st.total) mma_commit(&B.acc_full);
         }
         __syncwarp();
     }
@@ -1166,6 +1213,7 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
             mbar_init(smem_addr(&B.tail), 1);
             mbar_init(smem_addr(&B.xfull), 1);
             mbar_init(smem_addr(&B.acc_full), 1);
+            mbar_init(smem_addr(&B.off_full), 8);
             for (int t = 0; t < 2; ++t) {
                 mbar_init(smem_addr(&B.s_full[t]), 1);
                 mbar_init(smem_addr(&B.s_free[t]), BwdCols<DP, KEYS>::kAlias ? 1 : 4);
