@@ -187,6 +187,7 @@ struct AttnParams {
     float scale;
     HeadsPtr q, k, v, out, dout, dq, dk, dv;
     float *lse;                   // [Hq, Nq]
+    unsigned n_tiles;             // tiles of the grid
     int tiles;                    // query tiles of a block, 1 or 2 (forward)
     int pack;                     // query heads of a key head side by side in a tile's rows (forward; 1: none)
     int splits;                   // parts, a block each: of the key axis (forward), of the heads that share a key head (keys)
@@ -208,19 +209,44 @@ constexpr int kTile = 128;                  // rows of a tile: queries or keys
 constexpr int kChunkBytes = kTile * 128;    // 128 rows of 64 bf16, 128-byte swizzle
 constexpr float kLog2e = 1.4426950408889634f;
 
-// The tile of sequence rows that a block works on.  (Under a causal mask the blocks
-// with the most to do come first: the last query rows, the first key rows.)
+// The tile of sequence rows that a block works on.
 struct Work {
     int q0, lq, k0, lk;    // the sequence's rows; lq, lk >= 0
     int row;               // first row of the tile within the sequence, or -1: nothing to do
+    int h, z;              // head, and part (see AttnParams::splits)
 };
+
+// Tile, head and part of this block.  Blocks of one head follow one another, so that
+// its keys and values are in L2 for all of them; under a causal mask the blocks with
+// the most to do come first instead, over all heads and parts: the last query rows
+// (REVERSE), the first key rows.
+struct Place {
+    int tile, h, z;
+};
+template <bool REVERSE>
+__device__ __forceinline__ Place place_of(const AttnParams &P, int heads) {
+    const unsigned b = blockIdx.x, tiles = P.n_tiles;
+    Place p;
+    if (P.causal) {
+        const unsigned of_tile = heads * P.splits, t = b / of_tile, r = b - t * of_tile;
+        p.tile = REVERSE ? tiles - 1 - t : t;
+        p.z = r / heads;
+        p.h = r - p.z * heads;
+    } else {
+        const unsigned r = b / tiles;
+        p.tile = b - r * tiles;
+        p.z = r / heads;
+        p.h = r - p.z * heads;
+    }
+    return p;
+}
 
 // Tile `t` of the tiles of `rows` rows that cut the sequences of `cu`, one
 // sequence after the other; called by one whole warp.  There are at most
 // n / rows + n_seq tiles.
 __device__ __forceinline__ Work find_work(const AttnParams &P, bool by_key, int t, int rows) {
     const int lane = threadIdx.x & 31;
-    Work w = {0, 0, 0, 0, -1};
+    Work w = {0, 0, 0, 0, -1, 0, 0};
     for (int base = 0; base < P.n_seq; base += 32) {
         const int s = base + lane;
         int q0 = 0, q1 = 0, k0 = 0, k1 = 0, tiles = 0;     // both sides at once: one trip to memory
@@ -314,7 +340,12 @@ __host__ __device__ constexpr uint32_t idesc_b_mn(int M, int N) { return idesc_b
 // key head stand side by side in one tile, so its keys are read once for all of
 // them, and several blocks divide the key axis; a second kernel joins their parts.
 
-constexpr int kAttnThreads = 384;             // 168 registers each = 256 * 208 + 128 * 88
+constexpr int kAttnThreads = 384;
+// Registers: 384 threads are launched with 168 each, which the softmax warpgroups
+// and the others divide anew (256 * 208 + 128 * 88 = 384 * 168).  With 224 and 56
+// the backward kernels' loading and issuing warps spilled (head size 128: 1808 us
+// against 1660).
+constexpr int kLaunchRegs = 168, kRegsUp = 208, kRegsDown = 88;
 constexpr int kPolyOf4 = 1;                     // of four pairs of exponentials, how many the FMA pipes take
 
 template <int DP>
@@ -459,7 +490,7 @@ __device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, con
         tc_fence_after();
     }
     const float inv = 1.0f / l;
-    const int64_t at = (int64_t)head * P.Nq + w.q0 + i, part = (int64_t)blockIdx.z * P.Hq * P.Nq + at;
+    const int64_t at = (int64_t)head * P.Nq + w.q0 + i, part = (int64_t)w.z * P.Hq * P.Nq + at;
     __nv_bfloat16 *out = P.out.at(w.q0 + i, head);
 #pragma unroll
     for (int c = 0; c < DP / 16; ++c) {
@@ -677,9 +708,12 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     __shared__ FwdBars B;
     uint8_t *sq = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023), *ring = sq + 2 * S::kQ;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.y, hk = P.pack > 1 ? h : h / (P.Hq / P.Hkv), rows = kTile / P.pack;
+    const int rows = kTile / P.pack;
     if (warp == 9) {
-        const Work w = find_work(P, false, P.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x, P.tiles * rows);
+        const Place at = place_of<true>(P, P.pack > 1 ? P.Hkv : P.Hq);
+        Work w = find_work(P, false, at.tile, P.tiles * rows);
+        w.h = at.h;
+        w.z = at.z;
         if (lane == 0) {
             B.w = w;
             B.abort = 0;
@@ -709,6 +743,7 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const Work w = B.w;
+    const int h = w.h, hk = P.pack > 1 ? h : h / (P.Hq / P.Hkv);
     if (P.splits > 1) griddep_launch_dependents();          // the joining kernel
     if (w.row < 0) {                                        // more blocks than tiles
         if (warp == 8) tmem_dealloc(B.tmem, 512);
@@ -722,14 +757,14 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     const bool two = P.tiles > 1 && w.lq - w.row > rows;
     const int all0 = tiles_of(0), all1 = tiles_of(1), all = max(all0, all1);
     // ... and this block's part of them, from key kb on
-    const int from = (int)((int64_t)all * blockIdx.z / P.splits), to = (int)((int64_t)all * (blockIdx.z + 1) / P.splits);
+    const int from = (int)((int64_t)all * w.z / P.splits), to = (int)((int64_t)all * (w.z + 1) / P.splits);
     const int kb = from * KT, n_max = to - from;
     const int n0 = min(max(all0 - from, 0), n_max), n1 = min(max(all1 - from, 0), n_max);
     if (warp < 8) {
-        regs_up<208>();
+        regs_up<kRegsUp>();
         if (warp < 4 || two) fwd_softmax<DP>(P, B, w, warp >> 2, warp < 4 ? n0 : n1, warp < 4 ? n1 : n0, kb, h);
     } else {
-        regs_down<88>();
+        regs_down<kRegsDown>();
         if (warp == 8) fwd_load<DP>(P, B, w, mq, mk, mv, sq, ring, two, n_max, kb, h, hk);
         else if (warp < (two ? 11 : 10)) fwd_mma<DP>(B, w, sq, ring, warp - 9, warp == 9 ? n0 : n1, n_max, kb);
     }
@@ -827,7 +862,7 @@ template <bool KEYS>
 __device__ __forceinline__ Stream stream_of(const AttnParams &P, const Work &w, int h) {
     Stream st = {0, 0, 0, 0, 0};
     if (KEYS) {
-        const int share = P.Hq / P.Hkv, from = share * blockIdx.z / P.splits, to = share * (blockIdx.z + 1) / P.splits;
+        const int share = P.Hq / P.Hkv, from = share * w.z / P.splits, to = share * (w.z + 1) / P.splits;
         st.head = h * share + from;
         const int i0 = P.causal ? max(0, w.row - (w.lk - w.lq)) : 0;
         st.first = i0 / kStream;
@@ -1022,7 +1057,7 @@ __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const
             for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[0][8 * q + e]) * f;
             if (KEYS && P.splits > 1) {
                 float4 *dst = reinterpret_cast<float4 *>(
-                    P.part_out + ((((int64_t)blockIdx.z * 2 + g) * P.Nk + w.k0 + i) * P.Hkv + h) * P.D + 16 * c + 8 * q);
+                    P.part_out + ((((int64_t)w.z * 2 + g) * P.Nk + w.k0 + i) * P.Hkv + h) * P.D + 16 * c + 8 * q);
                 dst[0] = make_float4(v[0], v[1], v[2], v[3]);
                 dst[1] = make_float4(v[4], v[5], v[6], v[7]);
             } else {
@@ -1200,9 +1235,11 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
     uint8_t *kept = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023), *ring = kept + 2 * S::kKept;
     uint8_t *select = kept + S::kTiles, *stats = select + 2 * kSelect;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.y;
     if (warp == 9) {
-        const Work w = find_work(P, KEYS, P.causal && !KEYS ? gridDim.x - 1 - blockIdx.x : blockIdx.x, kTile);
+        const Place at = place_of<!KEYS>(P, KEYS ? P.Hkv : P.Hq);
+        Work w = find_work(P, KEYS, at.tile, kTile);
+        w.h = at.h;
+        w.z = at.z;
         if (lane == 0) {
             B.w = w;
             B.abort = 0;
@@ -1247,6 +1284,7 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
     __syncthreads();
     tc_fence_after();
     const Work w = B.w;
+    const int h = w.h;
     // the key kernel starts as the query kernel, whose statistics it reads, ends
     if (!KEYS) griddep_launch_dependents();
     if (KEYS && P.splits > 1) griddep_launch_dependents();  // the joining kernel
@@ -1257,10 +1295,10 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
     }
     const Stream st = stream_of<KEYS>(P, w, h);
     if (warp < 8) {
-        regs_up<208>();
+        regs_up<kRegsUp>();
         bwd_group<DP, KEYS>(P, B, w, st, warp >> 2, h);
     } else {
-        regs_down<88>();
+        regs_down<kRegsDown>();
         if (st.n > 0) {
             if (warp == 8) bwd_load<DP, KEYS>(P, B, w, st, mx0, mx1, my0, my1, kept, ring, stats, h);
             else if (warp < 11) bwd_scores<DP, KEYS>(B, st, kept, ring, select, stats, warp - 9);

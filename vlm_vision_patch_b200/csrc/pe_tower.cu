@@ -203,7 +203,7 @@ bool ready_to_launch(Kernel kern, size_t smem, int dev, std::atomic<uint64_t> &d
     if (done.load(std::memory_order_relaxed) & bit) return true;
     cudaFuncAttributes at;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
-        cudaFuncGetAttributes(&at, kern) != cudaSuccess || at.numRegs * kAttnThreads < 256 * 208 + 128 * 88)
+        cudaFuncGetAttributes(&at, kern) != cudaSuccess || at.numRegs < kLaunchRegs)
         return false;
     done.fetch_or(bit, std::memory_order_relaxed);
     return true;
@@ -352,11 +352,11 @@ pe_status pe_rope(pe_heads q, pe_heads k, pe_dtype dt, int64_t N, int Hq, int Hk
     P.pairs = (int)S;
     P.tail = (int)(D - 2 * S);
     P.sign = inverse ? -1.f : 1.f;
-    const double two_pi = 6.283185307179586476925286766559;
+    const double two_pi = 6.283185307179586476925286766559, log2_theta = std::log2(theta);
     for (int a = 0, i = 0; a < axes; ++a)
         for (int j = 0; j < sections[a]; ++j, ++i) {
             P.axis[i] = (uint8_t)a;
-            P.turns[i] = std::pow(theta, axial ? -(double)j / sections[a] : -(double)i / (double)S) / two_pi;
+            P.turns[i] = std::exp2(-(axial ? (double)j / sections[a] : (double)i / (double)S) * log2_theta) / two_pi;
         }
     cudaStream_t st = (cudaStream_t)stream;
     const int vec = rope_vec(P, es);
@@ -542,6 +542,10 @@ pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, 
     P.tiles = plan.tiles;
     P.pack = plan.pack;
     P.splits = plan.splits;
+    P.n_tiles = plan.blocks;
+    const int64_t all = (int64_t)plan.blocks * plan.rows * plan.splits;
+    if (all > INT32_MAX) return PE_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)all);
     if (plan.splits > 1) {
         if (!ws) return PE_ERR_INVALID_ARG;
         if (!aligned16(ws)) return PE_ERR_ALIGN;
@@ -560,7 +564,7 @@ pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, 
         auto kern = pe_attn_fwd_kernel<decltype(dp)::value>;
         static std::atomic<uint64_t> done{0};
         if (!ready_to_launch(kern, S::kSmem, a->dev, done)) return PE_ERR_CUDA;
-        kern<<<dim3(plan.blocks, plan.rows, (unsigned)plan.splits), kAttnThreads, S::kSmem, st>>>(mq, mk, mv, P);
+        kern<<<grid, kAttnThreads, S::kSmem, st>>>(mq, mk, mv, P);
         if (plan.splits > 1) {
             if (cudaGetLastError() != cudaSuccess) return PE_ERR_CUDA;
             return finish(launch_after(pe_attn_join_kernel, dim3((unsigned)(((int64_t)a->Hq * Nq + 7) / 8)), 256, 0, st, P));
@@ -604,6 +608,9 @@ pe_status pe_attention_backward(pe_attention *a, int n_seq, const int32_t *cu_q,
     P.lse = const_cast<float *>(lse);
     P.stat = static_cast<uint4 *>(ws);
     P.splits = plan_key_parts(a, n_seq, Nq, Nk);
+    P.n_tiles = max_tiles(Nk, n_seq, kTile);
+    if ((int64_t)max_tiles(Nq, n_seq, kTile) * a->Hq > INT32_MAX || (int64_t)P.n_tiles * a->Hkv * P.splits > INT32_MAX)
+        return PE_ERR_UNSUPPORTED;
     P.part_out = reinterpret_cast<float *>(P.stat + (int64_t)a->Hq * Nq);
     cudaStream_t st = (cudaStream_t)stream;
     CUtensorMap mq, mk, mv, md;
@@ -623,12 +630,15 @@ pe_status pe_attention_backward(pe_attention *a, int n_seq, const int32_t *cu_q,
             !ready_to_launch(dkv_kern, BwdShape<DP, true>::kSmem, a->dev, dkv_done))
             return PE_ERR_CUDA;
         if (Nq > 0) {
-            const dim3 grid(max_tiles(Nq, n_seq, kTile), (unsigned)a->Hq);
-            dq_kern<<<grid, kAttnThreads, BwdShape<DP, false>::kSmem, st>>>(mq, md, mk, mv, P);
+            AttnParams Pq = P;
+            Pq.splits = 1;
+            Pq.n_tiles = max_tiles(Nq, n_seq, kTile);
+            const dim3 grid(Pq.n_tiles * (unsigned)a->Hq);
+            dq_kern<<<grid, kAttnThreads, BwdShape<DP, false>::kSmem, st>>>(mq, md, mk, mv, Pq);
             if (cudaGetLastError() != cudaSuccess) return PE_ERR_CUDA;
         }
         if (Nk > 0) {
-            const dim3 grid(max_tiles(Nk, n_seq, kTile), (unsigned)a->Hkv, (unsigned)P.splits);
+            const dim3 grid(P.n_tiles * (unsigned)(a->Hkv * P.splits));
             const size_t smem = BwdShape<DP, true>::kSmem;
             if (Nq == 0) {
                 dkv_kern<<<grid, kAttnThreads, smem, st>>>(mk, mv, mq, md, P);

@@ -105,8 +105,8 @@ def vision_positions(grid_thw: Sequence[Sequence[int]], merge: int = 2, device=N
         with _on(dev, stream):
             return vision_positions(grid_thw, merge, dev)
     where = torch.device("cuda", dev)
-    pos = torch.empty((3, n), dtype=_I32, device=where)
-    cu = torch.empty(frames + 1, dtype=_I32, device=where)
+    pos = torch.empty(3, n, dtype=_I32, device=where)
+    cu = pos.new_empty(frames + 1)
     B.pe_vision_positions(grids, merge, pos.data_ptr(), cu.data_ptr(), _raw(dev))
     return pos, cu
 
