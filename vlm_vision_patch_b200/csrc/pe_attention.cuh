@@ -655,6 +655,7 @@ __device__ __forceinline__ void fwd_mma(FwdBars &B, const Work &w, uint8_t *sq, 
         if (one) mbar_arrive(smem_addr(&B.empty[r.at]));
         __syncwarp();
     };
+    const int left = w.lk - kb;
     bool ok = n_max == 0 || (warp_wait(&B.qfull, 0, abort) && wait_full());
     if (ok && n_max > 0) {
         tc_fence_after();
@@ -675,7 +676,7 @@ __device__ __forceinline__ void fwd_mma(FwdBars &B, const Work &w, uint8_t *sq, 
         if (!ok) break;
         tc_fence_after();
         if (j < n) {
-            const int steps = (min(w.lk - kb - j * KT, KT) + 15) / 16;
+            const int steps = (min(left - j * KT, KT) + 15) / 16;
             const uint32_t b = d_v + r.at * (S::kKv >> 4);
             if (one) {
                 mma_ts(to, tp, b, kDescHi, kIdO, j > 0);
@@ -823,13 +824,6 @@ struct BwdShape {
 };
 constexpr int kBwdMaxStages = 8;
 
-struct BwdBars {
-    uint64_t full[kBwdMaxStages], empty[kBwdMaxStages], tail, xfull, s_full[2], s_free[2], d_full[2], acc_done[2], acc_full, off_full, drain[3];
-    float off[2][kTile];                          // what delta is off by, each group's part
-    uint32_t tmem;
-    int abort;
-    Work w;
-};
 
 // `bytes` contiguous bytes to shared memory (both 16-byte aligned, a multiple of 16).
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
@@ -857,6 +851,15 @@ struct Stream {
 // first time only sums ds, which is what delta is off by.  (Beyond 256 keys it
 // moves dq's error by 1 part in 100 and would cost a third of the kernel.)
 constexpr int kSweepTwice = 4;
+
+struct BwdBars {
+    uint64_t full[kBwdMaxStages], empty[kBwdMaxStages], tail, xfull, s_full[2], s_free[2], d_full[2], acc_done[2], acc_full, off_full, drain[3];
+    float off[2][kTile];                          // what delta is off by, each group's part
+    uint32_t tmem;
+    int abort;
+    Work w;
+    Stream st;
+};
 
 template <bool KEYS>
 __device__ __forceinline__ Stream stream_of(const AttnParams &P, const Work &w, int h) {
@@ -915,7 +918,7 @@ __device__ __forceinline__ void bwd_chunk(const uint32_t (&s)[16], const uint32_
 // p and ds of every second streamed tile, then half of the results; the 128
 // threads of group g, one kept row each.
 template <int DP, bool KEYS>
-__device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const Work &w, const Stream &st, int g, int h) {
+__device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const Work &w, Stream st, int g, int h) {
     using T = BwdCols<DP, KEYS>;
     volatile int *abort = &B.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1070,7 +1073,7 @@ __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const
 
 // Loads (one warp): the kept tiles, then the streamed ones through the ring.
 template <int DP, bool KEYS>
-__device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const Work &w, const Stream &st,
+__device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const Work &w, Stream st,
                                          const CUtensorMap &mx0, const CUtensorMap &mx1, const CUtensorMap &my0,
                                          const CUtensorMap &my1, uint8_t *kept, uint8_t *ring, uint8_t *stats, int h) {
     using S = BwdShape<DP, KEYS>;
@@ -1141,7 +1144,7 @@ __device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const 
 // s and dp of every second streamed tile, buffer b (one warp each: while one waits
 // for room, the other keeps the tensor cores busy).
 template <int DP, bool KEYS>
-__device__ __forceinline__ void bwd_scores(BwdBars &B, const Stream &st, uint8_t *kept, uint8_t *ring, uint8_t *select,
+__device__ __forceinline__ void bwd_scores(BwdBars &B, Stream st, uint8_t *kept, uint8_t *ring, uint8_t *select,
                                            uint8_t *stats, int b) {
     using T = BwdCols<DP, KEYS>;
     using S = BwdShape<DP, KEYS>;
@@ -1180,7 +1183,7 @@ __device__ __forceinline__ void bwd_scores(BwdBars &B, const Stream &st, uint8_t
 
 // The sums over the streamed tiles (one warp).
 template <int DP, bool KEYS>
-__device__ __forceinline__ void bwd_sums(BwdBars &B, const Stream &st, uint8_t *ring, int y_len) {
+__device__ __forceinline__ void bwd_sums(BwdBars &B, Stream st, uint8_t *ring, int y_len) {
     using T = BwdCols<DP, KEYS>;
     using S = BwdShape<DP, KEYS>;
     constexpr uint32_t kOne = S::kOne, kIdA = idesc_b_mn(kTile, DP);
@@ -1242,6 +1245,7 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
         w.z = at.z;
         if (lane == 0) {
             B.w = w;
+            if (w.row >= 0) B.st = stream_of<KEYS>(P, w, w.h);
             B.abort = 0;
             for (int i = 0; i < S::kStages; ++i) {
                 mbar_init(smem_addr(&B.full[i]), 1);
@@ -1283,7 +1287,7 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const Work w = B.w;
+    const Work &w = B.w;                                    // in shared memory: registers are short
     const int h = w.h;
     // the key kernel starts as the query kernel, whose statistics it reads, ends
     if (!KEYS) griddep_launch_dependents();
@@ -1293,7 +1297,7 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
         if (warp == 8) tmem_dealloc(B.tmem, 512);
         return;
     }
-    const Stream st = stream_of<KEYS>(P, w, h);
+    const Stream &st = B.st;                                // (each role copies what its loop needs)
     if (warp < 8) {
         regs_up<kRegsUp>();
         bwd_group<DP, KEYS>(P, B, w, st, warp >> 2, h);
