@@ -542,6 +542,7 @@ pe_status pe_vision_positions(int n, const int32_t *grid_thw, int merge, int32_t
  *              strides), but no other overlap is allowed
  * angle = pos * rate, reduced in 64 bits; the turn is computed in fp32 and
  * rounded once.  Pointers need only the alignment of dt.
+ * The heads of an output must not overlap.
  * Requires 1 <= D <= 1024, 1 <= S <= PE_ROPE_MAX_PAIRS, 2 S <= D, 1 <= axes <=
  * PE_ROPE_MAX_AXES, theta > 0 and finite, N < 2^31, Hq >= 1, strides >= 0.
  * Errors: PE_ERR_INVALID_ARG, PE_ERR_SHAPE, PE_ERR_DTYPE, PE_ERR_ALIGN,
@@ -606,7 +607,7 @@ typedef struct pe_attention pe_attention;
 /*
  * pe_attention_create -- Hq query heads on Hkv key/value heads (Hq a multiple of
  * Hkv; query head h reads key head h / (Hq / Hkv)) of D elements, D a multiple
- * of 8, 8 <= D <= 128; scale > 0 and finite.  causal = 1: row i of a sequence
+ * of 8, 8 <= D <= 128; 1e-20 <= scale <= 1e20.  causal = 1: row i of a sequence
  * of lq queries and lk keys sees keys j <= i + lk - lq (the last row sees all).
  * Binds to the current CUDA device.  Errors: PE_ERR_INVALID_ARG,
  * PE_ERR_UNSUPPORTED, PE_ERR_CUDA.
@@ -630,7 +631,8 @@ int64_t pe_attention_workspace(const pe_attention *a, int n_seq, int64_t Nq, int
  *   lse        : dev fp32 [Hq, Nq], natural logarithm, or NULL
  *   ws         : dev, 16-byte aligned, at least pe_attention_workspace bytes
  * q, k, v, out must be 16-byte aligned with strides that are multiples of 8
- * elements and at least D (pe_heads), and smaller than 2^39 elements.  A row
+ * elements and at least D (pe_heads), and smaller than 2^39 elements; the heads
+ * of out must not overlap.  A row
  * that sees no key gets out = 0 and lse = -inf.  Rows of no sequence are left
  * as they were.  n_seq = 0 or Nq = 0: nothing is launched.
  * Errors: PE_ERR_INVALID_ARG, PE_ERR_SHAPE, PE_ERR_ALIGN, PE_ERR_UNSUPPORTED
@@ -647,7 +649,7 @@ pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, 
  *     dv_j = sum_i p_ij dout_i,  ds_ij = p_ij (dout_i . v_j - delta_i),
  *     dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,
  * the sums for dk and dv over the query heads that share the key head as well.
- *   dq : [Nq, Hq, D] bf16;  dk, dv : [Nk, Hkv, D] bf16, layouts as above.  None
+ *   dq : [Nq, Hq, D] bf16;  dk, dv : [Nk, Hkv, D] bf16, layouts as out's.  None
  *   may overlap an input.  Rows that see no key, and keys that no row sees, get
  *   zero gradients; rows of no sequence are left as they were.
  * Other arguments and errors as pe_attention_forward (lse not NULL).

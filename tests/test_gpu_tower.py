@@ -480,6 +480,40 @@ def test_attention_neighbours_do_not_leak():
         assert (a[n:] == 3.0).all() and (b[n:] == 3.0).all()
 
 
+@pytest.mark.parametrize("causal", [False, True])
+def test_attention_many_sequences(causal):
+    """Thousands of short and empty sequences: each finds its rows (and the boundaries
+    may begin and end inside the buffers)."""
+    D, H = 64, 2
+    g = torch.Generator().manual_seed(3)
+    ql = torch.randint(0, 5, (3000,), generator=g).tolist()
+    kl = [max(0, a + int(b)) for a, b in zip(ql, torch.randint(-1, 4, (3000,), generator=g))]
+    nq, nk, pre = sum(ql), sum(kl), 7
+    q, do = normal(100, pre + nq + 9, H, D, dtype=BF), normal(101, pre + nq + 9, H, D, dtype=BF)
+    k, v = normal(102, nk, H, D, dtype=BF), normal(103, nk, H, D, dtype=BF)
+    att = vp.Attention(H, H, D, causal=causal)
+    out, lse = att.forward(q, k, v, cu(ql) + pre, cu(kl), out=torch.full_like(q, 2.0))
+    dq, dk, dv = att.backward(do, q, k, v, out, lse, cu(ql) + pre, cu(kl), dq=torch.full_like(q, 2.0))
+    mid = slice(pre, pre + nq)
+    R, A = attention_ref(q[mid], k, v, ql, kl, causal, D ** -0.5, do[mid])
+    check_attention({"out": out[mid], "lse": lse[:, mid], "dq": dq[mid], "dk": dk, "dv": dv}, R, A, nq, nk)
+    for t in (out, dq):
+        assert (t[:pre] == 2).all() and (t[pre + nq:] == 2).all()
+
+
+def test_attention_empty_sides():
+    D, H = 64, 2
+    some, none = normal(104, 5, H, D, dtype=BF), torch.empty(0, H, D, dtype=BF, device=DEV)
+    att = vp.Attention(H, H, D)
+    zero, five = torch.zeros(2, dtype=torch.int32, device=DEV), cu((5,))
+    out, lse = att.forward(some, none, none, five, zero)               # no keys at all
+    dq, dk, dv = att.backward(some, some, none, none, out, lse, five, zero)
+    assert not out.any() and torch.isneginf(lse).all() and not dq.any() and dk.shape == dv.shape == (0, H, D)
+    out, lse = att.forward(none, some, some, zero, five)               # no queries
+    dq, dk, dv = att.backward(none, none, some, some, out, lse, zero, five)
+    assert out.shape == dq.shape == (0, H, D) and not dk.any() and not dv.any()
+
+
 def test_attention_divided_keys_leave_other_rows():
     """The joined form (one row on a long key axis) writes rows of sequences only."""
     D, H, n = 128, 2, 9000
@@ -640,6 +674,9 @@ def test_attention_refuses():
     assert e.value.status == "PE_ERR_ALIGN"
     with pytest.raises(PEError) as e:
         att.forward(x.flatten()[:64].expand(64, 2, 64), x, x, c)     # overlapping rows
+    assert e.value.status == "PE_ERR_SHAPE"
+    with pytest.raises(PEError) as e:                               # an output whose heads overlap
+        att.forward(x, x, x, c, out=torch.empty(64 * 128 + 64, dtype=BF, device=DEV).as_strided((64, 2, 64), (64, 64, 1)))
     assert e.value.status == "PE_ERR_SHAPE"
     for bad in ((3, 2, 64, 0.1), (2, 2, 12, 0.1), (2, 2, 64, 0.0), (2, 2, 64, math.inf), (0, 1, 64, 0.1)):
         with pytest.raises(PEError) as e:

@@ -48,7 +48,8 @@ ROPE = dict(q=h(), k=h(), dt=1, N=4, Hq=2, Hk=2, D=8, pos_ptr=P, sections=(4,), 
     (dict(N=2 ** 31), "PE_ERR_UNSUPPORTED"), (dict(dt=2), "PE_ERR_DTYPE"), (dict(pos_ptr=None), "PE_ERR_INVALID_ARG"),
     (dict(pos_ptr=P + 2), "PE_ERR_ALIGN"), (dict(q=h(None)), "PE_ERR_INVALID_ARG"), (dict(k_out=h(None)), "PE_ERR_INVALID_ARG"),
     (dict(q=h(P + 1)), "PE_ERR_ALIGN"), (dict(dt=0, q_out=h(P + 2)), "PE_ERR_ALIGN"),
-    (dict(q=h(P, -64)), "PE_ERR_INVALID_ARG"), (dict(N=0, pos_ptr=None, q=h(None)), "PE_OK"),
+    (dict(q=h(P, -64)), "PE_ERR_INVALID_ARG"), (dict(q_out=h(P, 8, 8)), "PE_ERR_SHAPE"),
+    (dict(k_out=h(P, 0, 8)), "PE_ERR_SHAPE"), (dict(k_out=h(P, 16, 4)), "PE_ERR_SHAPE"), (dict(N=0, pos_ptr=None, q=h(None)), "PE_OK"),
 ])
 def test_rope_refuses(change, want):
     assert status(B.pe_rope, *{**ROPE, **change}.values()) == want
@@ -113,7 +114,8 @@ def test_attention_create_refuses_before_any_device_call():
         a = ctypes.c_void_p(1)
         assert B.load().pe_attention_create(*bad, ctypes.byref(a)) == 1 and not a.value
     a = ctypes.c_void_p(1)
-    assert B.load().pe_attention_create(2, 2, 136, 0.1, 0, ctypes.byref(a)) == 7 and not a.value
+    for bad in ((2, 2, 136, 0.1, 0), (2, 2, 64, 1e-21, 0), (2, 2, 64, 1e21, 0)):
+        assert B.load().pe_attention_create(*bad, ctypes.byref(a)) == 7 and not a.value
     assert B.load().pe_attention_create(2, 2, 64, 0.1, 0, None) == 1
     assert B.pe_attention_last_error(None) == 1
     B.pe_attention_destroy(None)

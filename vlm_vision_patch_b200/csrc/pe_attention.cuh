@@ -241,40 +241,42 @@ __device__ __forceinline__ Place place_of(const AttnParams &P, int heads) {
     return p;
 }
 
-// Tile `t` of the tiles of `rows` rows that cut the sequences of `cu`, one
-// sequence after the other; called by one whole warp.  There are at most
-// n / rows + n_seq tiles.
+// Tile `t` of the tiles of `rows` rows that cut the sequences of one side; called by
+// one whole warp.  Sequence s has the tiles from F(s) = floor((cu[s] - cu[0]) / rows)
+// + s on: enough for its rows (F(s + 1) - F(s) >= ceil(length / rows)), at most one
+// too many, n / rows + n_seq in all, and F needs one boundary only, so that a tile
+// finds its sequence by search, 32 places at a time, however many there are.
 __device__ __forceinline__ Work find_work(const AttnParams &P, bool by_key, int t, int rows) {
     const int lane = threadIdx.x & 31;
-    Work w = {0, 0, 0, 0, -1, 0, 0};
-    for (int base = 0; base < P.n_seq; base += 32) {
-        const int s = base + lane;
-        int q0 = 0, q1 = 0, k0 = 0, k1 = 0, tiles = 0;     // both sides at once: one trip to memory
-        if (s < P.n_seq) {
+    const int32_t *cu = by_key ? P.cu_k : P.cu_q;
+    const int n = by_key ? P.Nk : P.Nq;
+    int lo = 0, hi = P.n_seq;                              // the sequence is in [lo, hi)
+    int q0 = 0, q1 = 0, k0 = 0, k1 = 0, first = 0;
+    while (true) {
+        const int step = (hi - lo + 31) / 32, s = lo + lane * step;
+        const bool there = s < hi;
+        const int c0 = boundary(cu, 0, n);
+        if (there && step == 1) {                          // the last look: all that the block needs
             q0 = boundary(P.cu_q, s, P.Nq), q1 = boundary(P.cu_q, s + 1, P.Nq);
             k0 = boundary(P.cu_k, s, P.Nk), k1 = boundary(P.cu_k, s + 1, P.Nk);
-            const int len = by_key ? k1 - k0 : q1 - q0;
-            tiles = len > 0 ? (len + rows - 1) / rows : 0;
         }
-        int sum = tiles;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += v;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, t < sum);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            w.q0 = __shfl_sync(0xffffffffu, q0, src);
-            w.lq = __shfl_sync(0xffffffffu, max(q1 - q0, 0), src);
-            w.k0 = __shfl_sync(0xffffffffu, k0, src);
-            w.lk = __shfl_sync(0xffffffffu, max(k1 - k0, 0), src);
-            w.row = (t - __shfl_sync(0xffffffffu, sum - tiles, src)) * rows;
+        const int c = !there ? 0 : (step > 1 ? boundary(cu, s, n) : (by_key ? k0 : q0));
+        first = (c - c0) / rows + s;
+        const unsigned hit = __ballot_sync(0xffffffffu, there && first <= t);
+        const int at = hit ? 31 - __clz(hit) : 0;
+        if (step == 1) {
+            Work w = {0, 0, 0, 0, -1, 0, 0};
+            w.q0 = __shfl_sync(0xffffffffu, q0, at);
+            w.lq = __shfl_sync(0xffffffffu, max(q1 - q0, 0), at);
+            w.k0 = __shfl_sync(0xffffffffu, k0, at);
+            w.lk = __shfl_sync(0xffffffffu, max(k1 - k0, 0), at);
+            const int64_t row = (int64_t)(t - __shfl_sync(0xffffffffu, first, at)) * rows;
+            if (row >= 0 && row < (by_key ? w.lk : w.lq)) w.row = (int)row;
             return w;
         }
-        t -= __shfl_sync(0xffffffffu, sum, 31);
+        lo += at * step;
+        hi = min(lo + step, hi);
     }
-    return w;
 }
 
 // A place in a ring of N stages, and the parity of its barriers' phase there.

@@ -43,6 +43,16 @@ int current_sms() {
     return n;
 }
 
+// Whether the heads of a tensor that is written do not overlap.
+bool disjoint(const pe_heads &t, int64_t rows, int heads, int D) {
+    const int64_t row = rows > 1 ? t.row_stride : INT64_MAX, head = heads > 1 ? t.head_stride : INT64_MAX;
+    const int64_t inner = std::min(row, head), count = row < head ? rows : heads;
+    if (inner == INT64_MAX) return true;                   // one row of one head
+    if (inner < D) return false;
+    const int64_t outer = std::max(row, head);
+    return outer == INT64_MAX || (outer - D) / inner >= count - 1;
+}
+
 // ------------------------------------------------------------- rotary positions
 
 // The widest access (at most 16 bytes) that divides the head's halves and tail,
@@ -226,8 +236,8 @@ cudaError_t launch_after(void (*kern)(K...), dim3 grid, int threads, size_t smem
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// Tiles of `rows` rows that n rows in n_seq sequences can make, at most.
-unsigned max_tiles(int64_t n, int n_seq, int rows) { return (unsigned)(n / rows + std::min<int64_t>(n_seq, n)); }
+// Tiles of `rows` rows that n rows in n_seq sequences are given (find_work).
+unsigned max_tiles(int64_t n, int n_seq, int rows) { return (unsigned)(n / rows + n_seq); }
 
 // Sizes that do not depend on the buffers.
 pe_status check_attention(const pe_attention *a, int n_seq, int64_t Nq, int64_t Nk) {
@@ -344,6 +354,7 @@ pe_status pe_rope(pe_heads q, pe_heads k, pe_dtype dt, int64_t N, int Hq, int Hk
         if (!aligned_to(in[i]->ptr, es) || !aligned_to(out[i]->ptr, es)) return PE_ERR_ALIGN;
         if (in[i]->row_stride < 0 || in[i]->head_stride < 0 || out[i]->row_stride < 0 || out[i]->head_stride < 0)
             return PE_ERR_INVALID_ARG;
+        if (!disjoint(*out[i], N, heads, D)) return PE_ERR_SHAPE;
         P.s[i] = {in[i]->ptr, out[i]->ptr, in[i]->row_stride, in[i]->head_stride, out[i]->row_stride,
                   out[i]->head_stride, heads};
     }
@@ -448,7 +459,7 @@ pe_status pe_attention_create(int Hq, int Hkv, int D, float scale, int causal, p
     if (Hq < 1 || Hkv < 1 || Hq % Hkv || D < 8 || D % 8 || !(scale > 0.f) || !std::isfinite(scale) ||
         (causal != 0 && causal != 1))
         return PE_ERR_INVALID_ARG;
-    if (D > 128 || Hq > 65535) return PE_ERR_UNSUPPORTED;
+    if (D > 128 || Hq > 65535 || scale < 1e-20f || scale > 1e20f) return PE_ERR_UNSUPPORTED;
     pe_attention *a = new (std::nothrow) pe_attention();
     if (!a) return PE_ERR_HOST_MEMORY;
     int major = 0, minor = 0;
@@ -528,6 +539,7 @@ pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, 
     const int D = a->D;
     for (const pe_status s : {check_heads(q, Nq, a->Hq, D), check_heads(out, Nq, a->Hq, D)})
         if (s != PE_OK) return s;
+    if (!disjoint(out, Nq, a->Hq, D)) return PE_ERR_SHAPE;
     if (Nk > 0)
         for (const pe_status s : {check_heads(k, Nk, a->Hkv, D), check_heads(v, Nk, a->Hkv, D)})
             if (s != PE_OK) return s;
@@ -590,11 +602,13 @@ pe_status pe_attention_backward(pe_attention *a, int n_seq, const int32_t *cu_q,
         for (const pe_status s : {check_heads(q, Nq, a->Hq, D), check_heads(out, Nq, a->Hq, D),
                                   check_heads(dout, Nq, a->Hq, D), check_heads(dq, Nq, a->Hq, D)})
             if (s != PE_OK) return s;
+        if (!disjoint(dq, Nq, a->Hq, D)) return PE_ERR_SHAPE;
     }
     if (Nk > 0)
         for (const pe_status s : {check_heads(k, Nk, a->Hkv, D), check_heads(v, Nk, a->Hkv, D),
                                   check_heads(dk, Nk, a->Hkv, D), check_heads(dv, Nk, a->Hkv, D)})
             if (s != PE_OK) return s;
+    if (Nk > 0 && (!disjoint(dk, Nk, a->Hkv, D) || !disjoint(dv, Nk, a->Hkv, D))) return PE_ERR_SHAPE;
     DeviceGuard g(a->dev);
     AttnParams P = attention_params(a, n_seq, cu_q, Nq, cu_k, Nk);
     P.q = heads_ptr(q, Nq, a->Hq);
