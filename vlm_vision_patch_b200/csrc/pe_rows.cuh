@@ -372,6 +372,7 @@ pe_norm_bwd_kernel(const NormParams P) {
     __shared__ float red[S::kThreads / 32];
     const int t = threadIdx.x % TPR, lane_row = threadIdx.x / TPR, chunks = P.E / (2 * kP);
     const float inv_e = 1.0f / (float)P.E;
+    if (P.part) griddep_launch_dependents();              // the summing kernel
     float2 dg[CPT][kP], db[CPT][kP], gm[CPT][kP];
     // gamma stays in registers: every row passing by would push it out of L1
 #pragma unroll
@@ -501,6 +502,7 @@ pe_norm_bwd_kernel(const NormParams P) {
 // warps every 32nd row each (four loads in flight), then the 32 sums in order.
 __global__ void __launch_bounds__(1024) pe_norm_sum_kernel(const float *part, int n, int E, int w_f32, void *dgamma,
                                                            void *dbeta) {
+    griddep_wait();                                       // for the kernel that wrote `part`
     __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;

@@ -43,6 +43,23 @@ int current_sms() {
     return n;
 }
 
+// A kernel that waits (griddepcontrol) for the one before it on the stream: its
+// blocks may start, and its set-up run, as that one's last blocks end.
+template <class... K, class... A>
+cudaError_t launch_after(void (*kern)(K...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Whether the heads of a tensor that is written do not overlap.
 bool disjoint(const pe_heads &t, int64_t rows, int heads, int D) {
     const int64_t row = rows > 1 ? t.row_stride : INT64_MAX, head = heads > 1 ? t.head_stride : INT64_MAX;
@@ -217,23 +234,6 @@ bool ready_to_launch(Kernel kern, size_t smem, int dev, std::atomic<uint64_t> &d
         return false;
     done.fetch_or(bit, std::memory_order_relaxed);
     return true;
-}
-
-// A kernel that waits (griddepcontrol) for the one before it on the stream: its
-// blocks may start, and its set-up run, as that one's last blocks end.
-template <class... K, class... A>
-cudaError_t launch_after(void (*kern)(K...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 // Tiles of `rows` rows that n rows in n_seq sequences are given (find_work).
@@ -449,8 +449,8 @@ pe_status pe_layernorm_backward(const void *dy, const void *x, pe_dtype dt, int6
         if (e != cudaSuccess) return PE_ERR_CUDA;
     }
     if (!dgamma) return PE_OK;
-    pe_norm_sum_kernel<<<(2 * E + 31) / 32, 1024, 0, st>>>(P.part, plan.blocks, E, P.w_f32, dgamma, dbeta);
-    return finish(cudaGetLastError());
+    return finish(launch_after(pe_norm_sum_kernel, dim3((unsigned)((2 * E + 31) / 32)), 1024, 0, st,
+                               (const float *)P.part, plan.blocks, E, P.w_f32, dgamma, dbeta));
 }
 
 pe_status pe_attention_create(int Hq, int Hkv, int D, float scale, int causal, pe_attention **out) {

@@ -52,27 +52,30 @@ def _raw(device: int) -> int:
 
 def _dense(t: torch.Tensor, name: str, device: int, shape=None, dtype: Optional[torch.dtype] = None) -> int:
     """Data pointer of a contiguous tensor on `device`."""
+    if (t.get_device() == device >= 0 and (shape is None or t.shape == shape)
+            and (dtype is None or t.dtype == dtype) and t.is_contiguous()):
+        return t.data_ptr()
+    _place(t, name, device)
+    if shape is not None:
+        _need(t, shape, name)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}; expected {dtype}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _place(t: torch.Tensor, name: str, device: int) -> None:
     if device < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}; expected cuda:{device}")
-    if shape is not None and t.shape != shape:
-        _need(t, shape, name)
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} is {t.dtype}; expected {dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
 
 
 def _heads(t: torch.Tensor, name: str, device: int, dtype: torch.dtype, shape) -> B.pe_heads:
     """A [rows, heads, D] tensor whose last axis is contiguous."""
-    if t.get_device() != device or device < 0:
-        raise ValueError(f"{name} is on {t.device}; expected cuda:{device}" if device >= 0
-                         else f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} is {t.dtype}; expected {dtype}")
-    if t.shape != shape:
+    if not (t.get_device() == device >= 0 and t.dtype == dtype and t.shape == shape):
+        _place(t, name, device)
+        if t.dtype != dtype:
+            raise TypeError(f"{name} is {t.dtype}; expected {dtype}")
         _need(t, shape, name)
     row, head, one = t.stride()
     if one != 1 and shape[2] > 1 and t.numel():
