@@ -153,10 +153,10 @@ constexpr int kRopeRows = 8;     // rows, and warps, of a block
 // a position of a million costs no accuracy, and 64 bits are spent on S values a
 // row, not on every element.  A lane keeps VEC of them in registers and takes the
 // same VEC pairs of one head after the other, the lanes as many heads side by side
-// as fit; two heads' loads are on their way ahead of the arithmetic, the first two
-// while the cosines are computed.
+// as fit; two or four heads' loads are on their way ahead of the arithmetic, the
+// first while the cosines are computed.
 template <class T, int VEC>
-__global__ void __launch_bounds__(32 * kRopeRows, sizeof(T) * VEC == 16 ? 4 : 6) pe_rope_kernel(const __grid_constant__ RopeParams P) {
+__global__ void __launch_bounds__(32 * kRopeRows, 4) pe_rope_kernel(const __grid_constant__ RopeParams P) {
     extern __shared__ float2 all[];                      // [kRopeRows][pairs] (cos, sin)
     using V = Pack<T, VEC>;
     const int S = P.pairs, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(32 * kRopeRows, sizeof(T) * VEC == 16 ? 4 : 6)
     T *out1 = static_cast<T *>(P.s[1].out) + row * P.s[1].out_row - heads0 * P.s[1].out_head;
     auto source = [&](int h) { return h < heads0 ? in0 + h * P.s[0].in_head : in1 + h * P.s[1].in_head; };
     auto target = [&](int h) { return h < heads0 ? out0 + h * P.s[0].out_head : out1 + h * P.s[1].out_head; };
-    V a[2], b[2];
+    constexpr int kAhead = sizeof(T) * VEC >= 16 ? 2 : 4;    // heads on their way
+    V a[kAhead], b[kAhead];
     auto fetch = [&](V &x, V &y, int h, int v) {
         if (h >= heads || h0 >= step) return;
         const T *p = source(h) + (v < sv ? v * VEC : S + v * VEC);           // the tail begins at 2 S
@@ -178,8 +179,8 @@ __global__ void __launch_bounds__(32 * kRopeRows, sizeof(T) * VEC == 16 ? 4 : 6)
         if (v < sv) y = *reinterpret_cast<const V *>(p + S);
     };
     int v = lane - h0 * across;
-    fetch(a[0], b[0], h0, v);
-    fetch(a[1], b[1], h0 + step, v);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) fetch(a[u], b[u], h0 + u * step, v);
     float2 *cs = all + warp * S;
     for (int p = lane; p < S; p += 32) {
         const double t = (double)P.pos[(int64_t)P.axis[p] * P.N + row] * P.turns[p];
@@ -195,9 +196,9 @@ __global__ void __launch_bounds__(32 * kRopeRows, sizeof(T) * VEC == 16 ? 4 : 6)
         float2 t[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) t[e] = turn ? cs[v * VEC + e] : make_float2(1.f, 0.f);
-        for (int h = h0; h < heads; h += 2 * step) {
+        for (int h = h0; h < heads; h += kAhead * step) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < kAhead; ++u) {
                 if (h + u * step >= heads) break;
                 T *o = target(h + u * step) + (turn ? v * VEC : S + v * VEC);
                 V x = a[u], y;
@@ -217,12 +218,12 @@ __global__ void __launch_bounds__(32 * kRopeRows, sizeof(T) * VEC == 16 ? 4 : 6)
                     *reinterpret_cast<V *>(o + S) = y;
                 }
                 *reinterpret_cast<V *>(o) = x;
-                fetch(a[u], b[u], h + (2 + u) * step, v);
+                fetch(a[u], b[u], h + (kAhead + u) * step, v);
             }
         }
         if (v + across < per_head) {
-            fetch(a[0], b[0], h0, v + across);
-            fetch(a[1], b[1], h0 + step, v + across);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) fetch(a[u], b[u], h0 + u * step, v + across);
         }
     }
 }
