@@ -294,6 +294,12 @@ def test_forward_protocol(stages):
         forward(seed, n0, None if seed % 3 == 0 else max(n0 + seed % 4 - 1, 0), stages)
 
 
+@pytest.mark.parametrize("stages", [4, 8])
+def test_forward_protocol_of_one_tile(stages):
+    for seed in range(100):
+        forward(seed, seed % 19, None, stages)
+
+
 def test_the_model_sees_planted_mistakes():
     def caught(**kw):
         for seed in range(400):

@@ -501,6 +501,38 @@ def test_attention_many_sequences(causal):
         assert (t[:pre] == 2).all() and (t[pre + nq:] == 2).all()
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,ql,kl,causal", [
+    (64, 16, 16, (64, 1, 130, 0, 63, 65, 200, 17, 128, 129, 5), None, False),
+    (80, 16, 16, (64,) * 12, None, False),
+    (72, 20, 20, (700, 12, 0, 128, 191, 1, 400), None, True),
+    (96, 24, 12, (300, 129, 31, 3, 70), (64, 65, 0, 450, 1), False),
+    (128, 24, 24, (40, 513, 64, 150), (30, 600, 64, 127), True),
+    (128, 64, 16, tuple(range(1, 13)), tuple(range(150, 30, -10)), True),
+    (8, 160, 160, (3, 0, 2), (66, 5, 300), False),
+])
+def test_attention_two_blocks_a_multiprocessor(D, Hq, Hkv, ql, kl, causal):
+    """Short sequences in so many tiles that blocks of one tile share an SM; one sequence
+    holds NaN, and the others' results do not."""
+    kl = ql if kl is None else kl
+    nq, nk = sum(ql), sum(kl)
+    q, do = normal(110, nq, Hq, D, dtype=BF), normal(113, nq, Hq, D, dtype=BF)
+    k, v = normal(111, nk, Hkv, D, dtype=BF), normal(112, nk, Hkv, D, dtype=BF)
+    att = vp.Attention(Hq, Hkv, D, causal=causal)
+    got = run_attention(att, q, k, v, do, cu(ql), cu(kl))
+    R, A = attention_ref(q, k, v, ql, kl, causal, D ** -0.5, do)
+    check_attention(got, R, A, nq, nk)
+    a, b = sum(ql[:2]), sum(ql[:3])
+    c, d = sum(kl[:2]), sum(kl[:3])
+    for t, lo, hi in ((q, a, b), (do, a, b), (k, c, d), (v, c, d)):
+        t[lo:hi] = math.nan
+    dirty = run_attention(att, q, k, v, do, cu(ql), cu(kl))
+    for n in ("out", "dq"):
+        assert torch.equal(dirty[n][:a], got[n][:a]) and torch.equal(dirty[n][b:], got[n][b:]), n
+    for n in ("dk", "dv"):
+        assert torch.equal(dirty[n][:c], got[n][:c]) and torch.equal(dirty[n][d:], got[n][d:]), n
+    assert torch.equal(dirty["lse"][:, :a], got["lse"][:, :a]) and torch.equal(dirty["lse"][:, b:], got["lse"][:, b:])
+
+
 def test_attention_empty_sides():
     D, H = 64, 2
     some, none = normal(104, 5, H, D, dtype=BF), torch.empty(0, H, D, dtype=BF, device=DEV)

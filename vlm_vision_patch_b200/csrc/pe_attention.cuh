@@ -338,6 +338,11 @@ __host__ __device__ constexpr uint32_t idesc_b_mn(int M, int N) { return idesc_b
 // only when a row's maximum has grown by more than 2^8, which keeps P in bf16's
 // range and is rare.
 //
+// Where sequences are short a block's start and end (its sequence's search, tensor
+// memory, first loads, last stores: about 8 us) cost more than its products: the
+// form with one tile (G = 1) is half as large in everything, so that two blocks
+// share an SM.  FwdPlan says when.
+//
 // With few query rows a sequence (a new token each, say) the heads that share a
 // key head stand side by side in one tile, so its keys are read once for all of
 // them, and several blocks divide the key axis; a second kernel joins their parts.
@@ -358,15 +363,20 @@ constexpr int kChunks = DP > 64 ? 2 : 1;
 template <int DP>
 constexpr int kKeys = DP <= 64 ? 128 : (DP <= 80 ? 112 : (DP <= 96 ? 96 : 80));
 
-template <int DP>
+// G query tiles a block.  With one (short sequences, below) two blocks share an SM:
+// half of tensor memory and of shared memory, 192 threads of 168 registers each,
+// and key tiles of 64.
+template <int DP, int G>
 struct FwdShape {
-    static constexpr int kC = kChunks<DP>, KT = kKeys<DP>;
+    static constexpr int kC = kChunks<DP>, KT = G == 1 ? 64 : kKeys<DP>;
+    static constexpr int kThreads = G == 1 ? 192 : kAttnThreads, kWarps = 4 * G;   // softmax warps
+    static constexpr uint32_t kCols = 256 * G;
     static constexpr int kChunk = KT * 128;                    // bytes of KT rows of 64 bf16
     static constexpr uint32_t kQ = kC * kChunkBytes, kKv = kC * kChunk;
-    static constexpr int kStages = DP <= 64 ? 8 : 5;
-    static constexpr size_t kSmem = 2 * kQ + (size_t)kStages * kKv + 1024;
-    static constexpr uint32_t kColS = 0, kColP = 2 * KT, kColO = 3 * KT;
-    static_assert(3 * KT + 2 * DP <= 512 && kSmem + 1024 <= 232448 && KT % 16 == 0, "on-chip memory");
+    static constexpr int kStages = DP <= 64 ? 8 : (G == 1 ? 4 : 5);
+    static constexpr size_t kSmem = G * kQ + (size_t)kStages * kKv + 1024;
+    static constexpr uint32_t kColS = 0, kColP = G * KT, kColO = G * KT * 3 / 2;
+    static_assert(G * (KT * 3 / 2 + DP) <= kCols && kSmem + 1024 <= 232448 * G / 2 && KT % 16 == 0, "on-chip memory");
 };
 
 struct FwdBars {
@@ -404,9 +414,9 @@ __device__ __forceinline__ float exp_row(const uint32_t (&s)[C][16], float sl2, 
 }
 
 // Online softmax of one 128-row tile; all 128 threads of its warps.
-template <int DP>
+template <int DP, int G>
 __device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, const Work &w, int tile, int n_kv, int n_other, int kb, int h) {
-    using S = FwdShape<DP>;
+    using S = FwdShape<DP, G>;
     constexpr int C = S::KT / 16;
     volatile int *abort = &B.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -570,11 +580,11 @@ __global__ void __launch_bounds__(256) pe_attn_join_kernel(const __grid_constant
 }
 
 // Loads (one warp): Q, then K0 K1 V0 K2 V1 ... (the order of use) through one ring.
-template <int DP>
+template <int DP, int G>
 __device__ __forceinline__ void fwd_load(const AttnParams &P, FwdBars &B, const Work &w, const CUtensorMap &mq,
                                          const CUtensorMap &mk, const CUtensorMap &mv, uint8_t *sq, uint8_t *ring, bool two,
                                          int n_max, int kb, int h, int hk) {
-    using S = FwdShape<DP>;
+    using S = FwdShape<DP, G>;
     constexpr int KT = S::KT;
     volatile int *abort = &B.abort;
     const int lane = threadIdx.x & 31;
@@ -628,10 +638,10 @@ __device__ __forceinline__ void fwd_load(const AttnParams &P, FwdBars &B, const 
 // read the last, P V when P is there.  Each tile has a warp of its own: the issuing
 // warp shares its instruction queue with the exponentials, and one warp for both
 // tiles spent longer queueing than the tensor cores working.
-template <int DP>
+template <int DP, int G>
 __device__ __forceinline__ void fwd_mma(FwdBars &B, const Work &w, uint8_t *sq, uint8_t *ring, int t, int n, int n_max,
                                         int kb) {
-    using S = FwdShape<DP>;
+    using S = FwdShape<DP, G>;
     constexpr int KT = S::KT;
     constexpr uint32_t kIdS = idesc_bf16_f32(kTile, KT), kIdO = idesc_b_mn(kTile, DP);
     volatile int *abort = &B.abort;
@@ -700,19 +710,20 @@ __device__ __forceinline__ void fwd_mma(FwdBars &B, const Work &w, uint8_t *sq, 
     if (!ok) drain_mmas(one, &B.drain[t]);
 }
 
-// mk, mv: boxes of kKeys rows; mq: of 128 / pack rows and pack heads.
-template <int DP>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+// mk, mv: boxes of FwdShape::KT rows; mq: of 128 / pack rows and pack heads.
+template <int DP, int G>
+__global__ void __launch_bounds__(G == 1 ? 192 : kAttnThreads, G == 1 ? 2 : 1)
 pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ AttnParams P) {
-    using S = FwdShape<DP>;
+    using S = FwdShape<DP, G>;
     constexpr int KT = S::KT;
     extern __shared__ uint8_t raw[];
     __shared__ FwdBars B;
-    uint8_t *sq = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023), *ring = sq + 2 * S::kQ;
+    uint8_t *sq = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023), *ring = sq + G * S::kQ;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = kTile / P.pack;
-    if (warp == 9) {
+    constexpr int kLoad = S::kWarps, kMma = kLoad + 1;      // the warps that load and (from kMma on) issue MMAs
+    if (warp == kMma) {
         const Place at = place_of<true>(P, P.pack > 1 ? P.Hkv : P.Hq);
         Work w = find_work(P, false, at.tile, P.tiles * rows);
         w.h = at.h;
@@ -720,7 +731,7 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         if (lane == 0) {
             B.w = w;
             B.abort = 0;
-            const int tiles = P.tiles > 1 && w.lq - w.row > rows ? 2 : 1;  // each gives a slot back
+            const int tiles = G > 1 && P.tiles > 1 && w.lq - w.row > rows ? 2 : 1;  // each gives a slot back
             for (int i = 0; i < S::kStages; ++i) mbar_init(smem_addr(&B.full[i]), 1), mbar_init(smem_addr(&B.empty[i]), tiles);
             mbar_init(smem_addr(&B.tail), 1);
             mbar_init(smem_addr(&B.qfull), 1);
@@ -738,8 +749,8 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             prefetch_tmap(&mv);
         }
     }
-    if (warp == 8) {
-        tmem_alloc(smem_addr(&B.tmem), 512);
+    if (warp == kLoad) {
+        tmem_alloc(smem_addr(&B.tmem), S::kCols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -749,7 +760,7 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     const int h = w.h, hk = P.pack > 1 ? h : h / (P.Hq / P.Hkv);
     if (P.splits > 1) griddep_launch_dependents();          // the joining kernel
     if (w.row < 0) {                                        // more blocks than tiles
-        if (warp == 8) tmem_dealloc(B.tmem, 512);
+        if (warp == kLoad) tmem_dealloc(B.tmem, S::kCols);
         return;
     }
     // key tiles that each query tile meets (the second tile may be missing) ...
@@ -757,27 +768,27 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         const int last = min(w.row + (t + 1) * rows, w.lq) - 1;
         return t < P.tiles && w.lq - w.row > t * rows ? (keys_seen(P, w, last) + KT - 1) / KT : 0;
     };
-    const bool two = P.tiles > 1 && w.lq - w.row > rows;
+    const bool two = G > 1 && P.tiles > 1 && w.lq - w.row > rows;
     const int all0 = tiles_of(0), all1 = tiles_of(1), all = max(all0, all1);
     // ... and this block's part of them, from key kb on
     const int from = (int)((int64_t)all * w.z / P.splits), to = (int)((int64_t)all * (w.z + 1) / P.splits);
     const int kb = from * KT, n_max = to - from;
     const int n0 = min(max(all0 - from, 0), n_max), n1 = min(max(all1 - from, 0), n_max);
-    if (warp < 8) {
-        regs_up<kRegsUp>();
-        if (warp < 4 || two) fwd_softmax<DP>(P, B, w, warp >> 2, warp < 4 ? n0 : n1, warp < 4 ? n1 : n0, kb, h);
+    if (warp < S::kWarps) {
+        if constexpr (G > 1) regs_up<kRegsUp>();
+        if (warp < 4 || two) fwd_softmax<DP, G>(P, B, w, warp >> 2, warp < 4 ? n0 : n1, warp < 4 ? n1 : n0, kb, h);
     } else {
-        regs_down<kRegsDown>();
-        if (warp == 8) fwd_load<DP>(P, B, w, mq, mk, mv, sq, ring, two, n_max, kb, h, hk);
-        else if (warp < (two ? 11 : 10)) fwd_mma<DP>(B, w, sq, ring, warp - 9, warp == 9 ? n0 : n1, n_max, kb);
+        if constexpr (G > 1) regs_down<kRegsDown>();
+        if (warp == kLoad) fwd_load<DP, G>(P, B, w, mq, mk, mv, sq, ring, two, n_max, kb, h, hk);
+        else if (warp < kMma + (two ? 2 : 1)) fwd_mma<DP, G>(B, w, sq, ring, warp - kMma, warp == kMma ? n0 : n1, n_max, kb);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && B.abort) atomicExch(P.err, (int)PE_ERR_DEVICE_TIMEOUT);
-    if (warp == 8) {
+    if (warp == kLoad) {
         tc_fence_after();
-        tmem_dealloc(B.tmem, 512);
+        tmem_dealloc(B.tmem, S::kCols);
     }
 }
 

@@ -220,17 +220,17 @@ auto with_head_size(int D, F &&f) {
     return f(std::integral_constant<int, 128>());
 }
 
-// Prepares an attention kernel of 384 threads whose warpgroups divide the
-// registers anew (setmaxnreg): more than it was launched with would be waited for
-// without end, so a build that gave it fewer is refused.  Once per kernel and
+// Prepares an attention kernel.  Where its warpgroups divide the registers anew
+// (setmaxnreg), more than it was launched with would be waited for without end, so
+// a build that gave it fewer than `regs` is refused.  Once per kernel and
 // device (`done`: a bit each); a second thread that does it again does no harm.
 template <class Kernel>
-bool ready_to_launch(Kernel kern, size_t smem, int dev, std::atomic<uint64_t> &done) {
+bool ready_to_launch(Kernel kern, size_t smem, int dev, std::atomic<uint64_t> &done, int regs = kLaunchRegs) {
     const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
     if (done.load(std::memory_order_relaxed) & bit) return true;
     cudaFuncAttributes at;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
-        cudaFuncGetAttributes(&at, kern) != cudaSuccess || at.numRegs < kLaunchRegs)
+        cudaFuncGetAttributes(&at, kern) != cudaSuccess || at.numRegs < regs)
         return false;
     done.fetch_or(bit, std::memory_order_relaxed);
     return true;
@@ -248,7 +248,7 @@ pe_status check_attention(const pe_attention *a, int n_seq, int64_t Nq, int64_t 
 
 // How a forward call lays its rows and keys out over blocks, from the sizes alone.
 struct FwdPlan {
-    int tiles, pack, splits;
+    int groups, tiles, pack, splits;   // groups of softmax warps and query tiles a block
     unsigned blocks, rows;       // blocks of one head and split; heads or, packed, key heads
 };
 
@@ -262,6 +262,12 @@ FwdPlan plan_forward(const pe_attention *a, int n_seq, int64_t Nq, int64_t Nk) {
     const int rows = kTile / p.pack;
     auto at_least = [&](int r) { return std::max<int64_t>((Nq + r - 1) / r, std::min<int64_t>(n_seq, Nq)) * p.rows; };
     p.tiles = at_least(2 * rows) * 2 <= a->num_sms ? 1 : 2;
+    // Short sequences: blocks of one tile, two a SM, hide each other's start and end (925
+    // sequences of 64 rows, 16 heads of 80: 815 -> 375 us; 115 of 512: 400 -> 339; 16 of 1024:
+    // 183 -> 170).  Longer ones would read their keys twice as often (16 of 2048, heads of
+    // 64: 492 -> 516), and fewer blocks than SMs would have less in flight each.
+    p.groups = Nq <= (int64_t)8 * rows * n_seq && at_least(rows) > a->num_sms ? 1 : 2;
+    if (p.groups == 1) p.tiles = 1;
     const int64_t blocks = at_least(p.tiles * rows);
     p.blocks = max_tiles(Nq, n_seq, p.tiles * rows);
     // With blocks for less than a quarter of the SMs the key axis is divided until there
@@ -566,22 +572,26 @@ pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, 
         P.part_lse2 = P.part_out + (int64_t)plan.splits * a->Hq * Nq * D;
     }
     cudaStream_t st = (cudaStream_t)stream;
-    return with_head_size(D, [&](auto dp) {
-        using S = FwdShape<decltype(dp)::value>;
+    auto run = [&](auto dp, auto groups) -> pe_status {
+        constexpr int DP = decltype(dp)::value, G = decltype(groups)::value;
+        using S = FwdShape<DP, G>;
         CUtensorMap mq, mk, mv;
         if (!make_heads_tmap(&mq, q, Nq, a->Hq, D, kTile / plan.pack, plan.pack)) return PE_ERR_CUDA;
         mk = mv = mq;                                       // without keys their maps are not read
         if (Nk > 0 && (!make_heads_tmap(&mk, k, Nk, a->Hkv, D, S::KT) || !make_heads_tmap(&mv, v, Nk, a->Hkv, D, S::KT)))
             return PE_ERR_CUDA;
-        auto kern = pe_attn_fwd_kernel<decltype(dp)::value>;
+        auto kern = pe_attn_fwd_kernel<DP, G>;
         static std::atomic<uint64_t> done{0};
-        if (!ready_to_launch(kern, S::kSmem, a->dev, done)) return PE_ERR_CUDA;
-        kern<<<grid, kAttnThreads, S::kSmem, st>>>(mq, mk, mv, P);
+        if (!ready_to_launch(kern, S::kSmem, a->dev, done, G == 1 ? 0 : kLaunchRegs)) return PE_ERR_CUDA;
+        kern<<<grid, S::kThreads, S::kSmem, st>>>(mq, mk, mv, P);
         if (plan.splits > 1) {
             if (cudaGetLastError() != cudaSuccess) return PE_ERR_CUDA;
             return finish(launch_after(pe_attn_join_kernel, dim3((unsigned)(((int64_t)a->Hq * Nq + 7) / 8)), 256, 0, st, P));
         }
         return finish(cudaGetLastError());
+    };
+    return with_head_size(D, [&](auto dp) {
+        return plan.groups == 1 ? run(dp, std::integral_constant<int, 1>()) : run(dp, std::integral_constant<int, 2>());
     });
 }
 
