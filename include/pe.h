@@ -632,9 +632,9 @@ int64_t pe_attention_workspace(const pe_attention *a, int n_seq, int64_t Nq, int
  *   ws         : dev, 16-byte aligned, at least pe_attention_workspace bytes
  * q, k, v, out must be 16-byte aligned with strides that are multiples of 8
  * elements and at least D (pe_heads), and smaller than 2^39 elements; the heads
- * of out must not overlap.  A row
- * that sees no key gets out = 0 and lse = -inf.  Rows of no sequence are left
- * as they were.  n_seq = 0 or Nq = 0: nothing is launched.
+ * of out must not overlap.  A row that sees no key gets out = 0 and lse = -inf;
+ * one that sees keys, all with scores of -inf, out = NaN and lse = -inf.  Rows
+ * of no sequence are left as they were.  n_seq = 0 or Nq = 0: nothing is launched.
  * Errors: PE_ERR_INVALID_ARG, PE_ERR_SHAPE, PE_ERR_ALIGN, PE_ERR_UNSUPPORTED
  * (Nq or Nk >= 2^31), PE_ERR_CUDA.
  */

@@ -413,6 +413,10 @@ __device__ __forceinline__ float exp_row(const uint32_t (&s)[C][16], float sl2, 
     return t.x + t.y;
 }
 
+// In place of the lse of a part whose keys a row sees, all with scores of -inf (a part
+// of which it sees no key has -inf itself).
+constexpr float kNoFiniteScore = -3.402823466e38f;
+
 // Online softmax of one 128-row tile; all 128 threads of its warps.
 template <int DP, int G>
 __device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, const Work &w, int tile, int n_kv, int n_other, int kb, int h) {
@@ -501,7 +505,9 @@ __device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, con
         if (!warp_wait(&B.pv_done[tile], (n_kv - 1) & 1, abort)) return;
         tc_fence_after();
     }
-    const float inv = 1.0f / l;
+    // A row that sees keys, all with scores of -inf, is NaN as in the formula (exp(-inf - -inf)); its l is
+    // not used, as the polynomial's least power of 2 is not 0.
+    const float inv = m == -INFINITY ? NAN : 1.0f / l;
     const int64_t at = (int64_t)head * P.Nq + w.q0 + i, part = (int64_t)w.z * P.Hq * P.Nq + at;
     __nv_bfloat16 *out = P.out.at(w.q0 + i, head);
 #pragma unroll
@@ -528,8 +534,10 @@ __device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, con
         }
     }
     if (!mine) return;
-    if (P.splits > 1) P.part_lse2[part] = limit > 0 ? m * sl2 + log2f(l) : -INFINITY;
-    else if (P.lse) P.lse[at] = limit > 0 ? m * P.scale + logf(l) : -INFINITY;
+    if (P.splits > 1) {
+        const float v = m * sl2 + log2f(l);
+        P.part_lse2[part] = limit <= 0 ? -INFINITY : (v == -INFINITY ? kNoFiniteScore : v);
+    } else if (P.lse) P.lse[at] = limit > 0 ? m * P.scale + logf(l) : -INFINITY;
 }
 
 // Whether row r belongs to a sequence of `cu`.
@@ -543,7 +551,8 @@ __device__ __forceinline__ bool in_sequence(const int32_t *cu, int n_seq, int n,
 }
 
 // Joins the parts of a row and head (one warp each): out = sum_z w_z out_z / sum_z
-// w_z with w_z = 2^(lse2_z - max).
+// w_z with w_z = 2^(lse2_z - max).  Parts without a finite score weigh nothing beside
+// others; a row of such parts only takes their NaN.
 __global__ void __launch_bounds__(256) pe_attn_join_kernel(const __grid_constant__ AttnParams P) {
     griddep_wait();
     const int lane = threadIdx.x & 31;
@@ -576,7 +585,8 @@ __global__ void __launch_bounds__(256) pe_attn_join_kernel(const __grid_constant
     if (4 * lane < P.D)
         *reinterpret_cast<uint2 *>(P.out.at(r, h) + 4 * lane) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (lane == 0 && P.lse) P.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) / kLog2e;
+    const float lse2 = top + log2f(sum);
+    if (lane == 0 && P.lse) P.lse[at] = sum == 0.f || lse2 <= 0.5f * kNoFiniteScore ? -INFINITY : lse2 / kLog2e;
 }
 
 // Loads (one warp): Q, then K0 K1 V0 K2 V1 ... (the order of use) through one ring.
