@@ -600,7 +600,8 @@ int64_t pe_layernorm_backward_workspace(int64_t N, int E);
  *     out_i = sum_j exp(s_ij - lse_i) v_j.
  * bf16 operands on the tensor cores, fp32 scores, statistics and sums; the
  * probabilities (and, in the gradient, their derivatives) are rounded to bf16
- * as operands of the second product.
+ * as operands of the second product.  The sums run over the rows seen alone: a NaN
+ * or an infinity in a row that the mask hides reaches no result.
  */
 typedef struct pe_attention pe_attention;
 

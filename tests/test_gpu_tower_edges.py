@@ -53,3 +53,65 @@ def test_rows_whose_every_score_is_minus_infinity(D, Hq, Hkv, ql, kl):
     # D products in fp32, their sum's and lse's roundings
     tol = D * 2.0 ** -23 * (q[0].double().abs() * k[one].double().repeat_interleave(share, 0).abs()).sum(-1) + 2.0 ** -22
     close(lse[:, 0], s, tol, "lse")
+
+
+# ------------------------------------------------------------------ masked places that are not finite
+
+
+CAUSAL = [
+    # D, Hq, Hkv, query lengths, key lengths, poisoned (sequence, row from its end)
+    (80, 2, 2, (700,), (700,), (0, 401)),
+    (64, 2, 1, (300, 515), (300, 515), (1, 130)),
+    (128, 4, 2, (513,), (600,), (0, 77)),
+    (96, 1, 1, (200,), (130,), (0, 60)),                      # early rows see no key
+    (72, 20, 20, (128, 100, 191, 65), (128, 100, 191, 65), (2, 100)),   # blocks of one tile
+    (128, 12, 2, (2, 3), (5000, 3000), (1, 1)),               # heads packed, the key axis divided
+    (64, 8, 8, (2,), (6000,), (0, 1)),
+    (8, 1, 1, (140,), (140,), (0, 7)),
+]
+
+
+@pytest.mark.parametrize("where,value", [("k", math.nan), ("v", math.nan), ("v", math.inf), ("v", -math.inf), ("q", math.nan),
+                                         ("do", math.nan), ("do", math.inf), ("q", math.inf)])
+@pytest.mark.parametrize("D,Hq,Hkv,ql,kl,at", CAUSAL)
+def test_causal_rows_do_not_see_later_rows(D, Hq, Hkv, ql, kl, at, where, value):
+    """A NaN or an infinity in a row that the mask hides reaches no result: neither the
+    outputs and gradients of earlier queries (from a key or value) nor the gradients
+    of later keys (from a query or its gradient)."""
+    nq, nk = sum(ql), sum(kl)
+    q, do = normal(10, nq, Hq, D, dtype=BF), normal(13, nq, Hq, D, dtype=BF)
+    k, v = normal(11, nk, Hkv, D, dtype=BF), normal(12, nk, Hkv, D, dtype=BF)
+    R, A = attention_ref(q, k, v, ql, kl, True, D ** -0.5, do)
+    s, back = at
+    q0, k0, lq, lk = sum(ql[:s]), sum(kl[:s]), ql[s], kl[s]
+    x = {"q": q, "k": k, "v": v, "do": do}[where]
+    t = (lk if where in "kv" else lq) - back
+    c = min(2, D // 8)
+    x[(k0 if where in "kv" else q0) + t, :, 5 * c:5 * c + 1] = value       # one element of every head
+    got = run_attention(vp.Attention(Hq, Hkv, D, causal=True), q, k, v, do, cu(ql), cu(kl))
+    # rows of this sequence that see the poisoned one: queries from `first` on, keys before `last`
+    if where in ("k", "v"):
+        first, last = max(t - (lk - lq), 0), lk if where == "k" else lk
+    else:
+        first, last = lq, min(t + lk - lq + 1, lk)
+    rows = torch.ones(nq, dtype=torch.bool, device=DEV)
+    cols = torch.ones(nk, dtype=torch.bool, device=DEV)
+    if where in ("k", "v"):
+        rows[q0 + first:q0 + lq] = False
+    else:
+        rows[q0 + t] = False
+    cols[k0:k0 + last] = False
+    assert rows.any()
+    for n, keep in (("out", rows), ("dq", rows), ("dk", cols), ("dv", cols)):
+        if keep.any():
+            close(got[n][keep], R[n][keep], A[n][keep] + U[BF] * R[n][keep].abs() + 1e-30, n)
+    if where == "do":
+        close(got["out"], R["out"], A["out"] + U[BF] * R["out"].abs(), "out")
+    # ... and who sees it is not spared
+    if where == "v":
+        hit = got["out"][q0 + first:q0 + lq, :, 5 * c]
+        assert not hit.isfinite().any()
+    if where == "do":
+        assert not got["dv"][k0:k0 + last, :, 5 * c].isfinite().any()
+    if math.isnan(value) and where == "q":
+        assert got["out"][q0 + t].isnan().all() and got["dk"][k0:k0 + last].isnan().all()

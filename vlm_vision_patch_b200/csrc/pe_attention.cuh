@@ -326,6 +326,67 @@ constexpr uint32_t kDescHiFlat = (128u >> 4) | (1u << 14);
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | ((uint32_t)kLayoutSw128 << 29);
 __host__ __device__ constexpr uint32_t idesc_b_mn(int M, int N) { return idesc_bf16_f32(M, N) | (1u << 16); }
 
+// ------------------------------------------------------------- hidden rows
+//
+// Under a causal mask a tile holds rows that some rows of the other side do not see.
+// In the products over the tile they meet probabilities of 0, and 0 times a NaN or an
+// infinity is not 0.  A result that is not finite is therefore looked at again, a warp
+// a row: if a hidden row holds such a value in one of its columns, the column is summed
+// anew over the rows seen, in fp32 without the tensor cores.  Only warps with rows that
+// the mask cuts look, in kernels of their own: with this code behind it the unmasked
+// forward loop took 7% longer (registers).
+
+// Whether an element of this thread's row in N times 16 columns of tensor memory, `step`
+// apart, is NaN or infinite; of the last only while `left` goes.
+template <int N>
+__device__ __forceinline__ bool tmem_odd(uint32_t taddr, int step, int left = 2 * N) {
+    float odd = 0.f;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+        if (2 * c >= left) break;
+        uint32_t o[1][16];
+        tmem_ld_x16(taddr + c * step, o[0]);
+        tmem_ld_wait_for(o);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) odd = fmaf(__uint_as_float(o[0][e]), 0.f, odd);
+    }
+    return !(odd == 0.f);
+}
+// Elements 4 lane .. 4 lane + 3 of a row of D, 0 behind it.
+__device__ __forceinline__ float4 quad(const __nv_bfloat16 *row, int D) {
+    const int e = 4 * (threadIdx.x & 31);
+    if (e >= D) return make_float4(0.f, 0.f, 0.f, 0.f);
+    const uint2 u = *reinterpret_cast<const uint2 *>(row + e);
+    return make_float4(bf16lo_to_f32(u.x), bf16hi_to_f32(u.x), bf16lo_to_f32(u.y), bf16hi_to_f32(u.y));
+}
+// The product of two rows, the same in every lane.
+__device__ __forceinline__ float quad_dot(float4 a, float4 b) {
+    float s = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, a.w * b.w)));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+__device__ __forceinline__ void quad_add(float4 &acc, float f, float4 v) {
+    acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y), acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
+}
+// Whether an element is NaN or infinite.
+__device__ __forceinline__ bool quad_odd(float4 v) {
+    return !(fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, v.w * 0.f))) == 0.f);
+}
+// Every 64th step: whether all columns to be summed anew are NaN already, as those are
+// that belong to rows seen.
+__device__ __forceinline__ bool quad_lost(int step, bool hit, float4 acc) {
+    if ((step & 63) != 63) return false;
+    const bool nan = acc.x != acc.x && acc.y != acc.y && acc.z != acc.z && acc.w != acc.w;
+    return __all_sync(0xffffffffu, !hit || nan);
+}
+// f * acc to this lane's columns of a row, as bf16, or as fp32 in a part.
+__device__ __forceinline__ void quad_store(__nv_bfloat16 *row, float *part, float f, float4 v) {
+    const int e = 4 * (threadIdx.x & 31);
+    if (part) *reinterpret_cast<float4 *>(part + e) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+    else *reinterpret_cast<uint2 *>(row + e) = make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+}
+
 // ------------------------------------------------------------- forward
 //
 // A block takes 256 query rows of one sequence and head as two tiles of 128 (one
@@ -384,6 +445,7 @@ struct FwdBars {
     uint32_t tmem;
     int abort;
     Work w;
+    volatile int keys[4 * 2][2];                 // per softmax warp: this block's first key and keys behind it, for the end
 };
 
 // MMAs in flight finish before their tensor memory is freed.
@@ -418,7 +480,7 @@ __device__ __forceinline__ float exp_row(const uint32_t (&s)[C][16], float sl2, 
 constexpr float kNoFiniteScore = -3.402823466e38f;
 
 // Online softmax of one 128-row tile; all 128 threads of its warps.
-template <int DP, int G>
+template <int DP, int G, bool CAUSAL>
 __device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, const Work &w, int tile, int n_kv, int n_other, int kb, int h) {
     using S = FwdShape<DP, G>;
     constexpr int C = S::KT / 16;
@@ -435,6 +497,7 @@ __device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, con
     const bool mine = i < w.lq && r < rows * P.pack;
     const int limit = mine ? keys_seen(P, w, i) - kb : INT32_MAX;  // of this block's keys
     const float sl2 = P.scale * kLog2e;
+    if (CAUSAL && lane == 0) B.keys[warp][0] = w.k0 + kb, B.keys[warp][1] = w.lk - kb;   // not in registers meanwhile
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n_kv; ++j) {
         if (!warp_wait(&B.s_full[tile], j & 1, abort)) return;
@@ -531,6 +594,35 @@ __device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, con
                 st_global_v4(out + 16 * c + 8 * g, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
             }
+        }
+    }
+    if constexpr (CAUSAL) {
+        // keys of this block's tiles from `limit` on are hidden from the row: fewer for every later one
+        __syncwarp();
+        const int k0 = B.keys[warp][0], end = min(B.keys[warp][1], n_kv * S::KT);
+        const bool some = mine && limit > 0 && limit < end && l < INFINITY && m > -INFINITY;
+        uint32_t again = 0;
+        if (__any_sync(0xffffffffu, some)) {
+            const bool lost = tmem_odd<DP / 16>(to, 16);               // (the whole warp)
+            again = __ballot_sync(0xffffffffu, some && lost);
+        }
+        int looked = end;
+        bool hit = false;
+        __syncwarp();
+        while (again) {
+            const int src = 31 - __clz(again), seen = __shfl_sync(0xffffffffu, limit, src);
+            again ^= 1u << src;
+            const int row = w.q0 + __shfl_sync(0xffffffffu, i, src), a_head = __shfl_sync(0xffffffffu, head, src);
+            const int kv = a_head / (P.Hq / P.Hkv);
+            const float base = __shfl_sync(0xffffffffu, m * sl2, src), f = __shfl_sync(0xffffffffu, inv, src);
+            while (looked > seen) hit |= quad_odd(quad(P.v.at(k0 + --looked, kv), P.D));
+            if (!__any_sync(0xffffffffu, hit)) continue;
+            const float4 q = quad(P.q.at(row, a_head), P.D);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j = 0; j < seen && !quad_lost(j, hit, acc); ++j)
+                quad_add(acc, ex2(fmaf(quad_dot(q, quad(P.k.at(k0 + j, kv), P.D)), sl2, -base)), quad(P.v.at(k0 + j, kv), P.D));
+            const int64_t to_part = (((int64_t)w.z * P.Hq + a_head) * P.Nq + row) * P.D;
+            if (hit) quad_store(P.out.at(row, a_head), P.splits > 1 ? P.part_out + to_part : nullptr, f, acc);
         }
     }
     if (!mine) return;
@@ -721,7 +813,7 @@ __device__ __forceinline__ void fwd_mma(FwdBars &B, const Work &w, uint8_t *sq, 
 }
 
 // mk, mv: boxes of FwdShape::KT rows; mq: of 128 / pack rows and pack heads.
-template <int DP, int G>
+template <int DP, int G, bool CAUSAL>
 __global__ void __launch_bounds__(G == 1 ? 192 : kAttnThreads, G == 1 ? 2 : 1)
 pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ AttnParams P) {
@@ -786,7 +878,7 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     const int n0 = min(max(all0 - from, 0), n_max), n1 = min(max(all1 - from, 0), n_max);
     if (warp < S::kWarps) {
         if constexpr (G > 1) regs_up<kRegsUp>();
-        if (warp < 4 || two) fwd_softmax<DP, G>(P, B, w, warp >> 2, warp < 4 ? n0 : n1, warp < 4 ? n1 : n0, kb, h);
+        if (warp < 4 || two) fwd_softmax<DP, G, CAUSAL>(P, B, w, warp >> 2, warp < 4 ? n0 : n1, warp < 4 ? n1 : n0, kb, h);
     } else {
         if constexpr (G > 1) regs_down<kRegsDown>();
         if (warp == kLoad) fwd_load<DP, G>(P, B, w, mq, mk, mv, sq, ring, two, n_max, kb, h, hk);
@@ -940,7 +1032,7 @@ __device__ __forceinline__ void bwd_chunk(const uint32_t (&s)[16], const uint32_
 
 // p and ds of every second streamed tile, then half of the results; the 128
 // threads of group g, one kept row each.
-template <int DP, bool KEYS>
+template <int DP, bool KEYS, bool CAUSAL>
 __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const Work &w, Stream st, int g, int h) {
     using T = BwdCols<DP, KEYS>;
     volatile int *abort = &B.abort;
@@ -1090,6 +1182,57 @@ __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const
                 st_global_v4(out + 16 * c + 8 * q, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
             }
+        }
+    }
+    if (!CAUSAL || st.n == 0) return;
+    // Streamed rows that the mask hides from a kept one: keys from `limit` on (fewer for every
+    // later query), queries before i - shift (more for every later key).
+    const int hidden = KEYS ? i - shift : limit, edge = KEYS ? st.first * kStream : min(st.n * kStream, w.lk);
+    const bool whole = KEYS || (nlse2 - nlse2 == 0.f && ndelta - ndelta == 0.f);
+    const bool some = mine && whole && (KEYS ? edge < hidden : hidden < edge);
+    if (!__any_sync(0xffffffffu, some)) return;
+    const bool lost = KEYS ? tmem_odd<DP / 16>(acc, 16) : tmem_odd<(DP / 16 + 1) / 2>(acc + 16 * g, 32, DP / 16 - g);
+    uint32_t again = __ballot_sync(0xffffffffu, some && lost);
+    int looked = edge;
+    bool hit = false;
+    __syncwarp();
+    while (again) {
+        const int src = KEYS ? __ffs(again) - 1 : 31 - __clz(again);
+        again ^= 1u << src;
+        const int row = (KEYS ? w.k0 : w.q0) + w.row + (warp & 3) * 32 + src, to = __shfl_sync(0xffffffffu, hidden, src);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (KEYS) {
+            const int heads = st.n / st.per_head;
+            for (; looked < to; ++looked)
+                for (int y = st.head; y < st.head + heads; ++y)
+                    hit |= quad_odd(quad((is_dv ? P.dout : P.q).at(w.q0 + looked, y), P.D));
+            if (!__any_sync(0xffffffffu, hit)) continue;
+            const float4 k = quad(P.k.at(row, h), P.D), v = quad(P.v.at(row, h), P.D);
+            for (int y = st.head; y < st.head + heads; ++y)
+                for (int r = to; r < w.lq && !quad_lost(r, hit, sum); ++r) {
+                    const uint4 t = P.stat[(int64_t)y * P.Nq + w.q0 + r];
+                    const float4 q = quad(P.q.at(w.q0 + r, y), P.D), dy = quad(P.dout.at(w.q0 + r, y), P.D);
+                    const float nl = bf16lo_to_f32(t.x) + bf16hi_to_f32(t.x) + bf16lo_to_f32(t.y);
+                    const float nd = bf16lo_to_f32(t.z) + bf16hi_to_f32(t.z) + bf16lo_to_f32(t.w);
+                    const float p = ex2((quad_dot(q, k) + nl) * sl2.x);
+                    if (is_dv) quad_add(sum, p, dy);
+                    else quad_add(sum, p * (quad_dot(dy, v) + nd), q);
+                }
+            float *part = P.part_out + ((((int64_t)w.z * 2 + g) * P.Nk + row) * P.Hkv + h) * P.D;
+            if (hit) quad_store((is_dv ? P.dv : P.dk).at(row, h), P.splits > 1 ? part : nullptr, f, sum);
+        } else {
+            const int kv = h / (P.Hq / P.Hkv);
+            const float nl = __shfl_sync(0xffffffffu, nlse2, src), nd = __shfl_sync(0xffffffffu, ndelta, src);
+            // (the other group has the other columns)
+            while (looked > to) hit |= quad_odd(quad(P.k.at(w.k0 + --looked, kv), P.D)) && ((lane >> 2) & 1) == g;
+            if (!__any_sync(0xffffffffu, hit)) continue;
+            const float4 q = quad(P.q.at(row, h), P.D), dy = quad(P.dout.at(row, h), P.D);
+            for (int j = 0; j < to && !quad_lost(j, hit, sum); ++j) {
+                const float4 k = quad(P.k.at(w.k0 + j, kv), P.D), v = quad(P.v.at(w.k0 + j, kv), P.D);
+                const float p = ex2(fmaf(quad_dot(q, k), sl2.x, nl));
+                quad_add(sum, p * (quad_dot(dy, v) + nd), k);
+            }
+            if (hit) quad_store(P.dq.at(row, h), nullptr, f, sum);
         }
     }
 }
@@ -1250,7 +1393,7 @@ __device__ __forceinline__ void bwd_sums(BwdBars &B, Stream st, uint8_t *ring, i
 }
 
 // mx0, mx1: maps of the kept tensors, my0, my1 of the streamed ones (boxes of 64 rows).
-template <int DP, bool KEYS>
+template <int DP, bool KEYS, bool CAUSAL>
 __global__ void __launch_bounds__(kAttnThreads, 1)
 pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constant__ CUtensorMap mx1,
                    const __grid_constant__ CUtensorMap my0, const __grid_constant__ CUtensorMap my1,
@@ -1315,7 +1458,7 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
     // the key kernel starts as the query kernel, whose statistics it reads, ends
     if (!KEYS) griddep_launch_dependents();
     if (KEYS && P.splits > 1) griddep_launch_dependents();  // the joining kernel
-    if (KEYS && warp == 8) griddep_wait();
+    if (KEYS) griddep_wait();                               // (before any bounded wait)
     if (w.row < 0) {                                        // more blocks than tiles
         if (warp == 8) tmem_dealloc(B.tmem, 512);
         return;
@@ -1323,7 +1466,7 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
     const Stream &st = B.st;                                // (each role copies what its loop needs)
     if (warp < 8) {
         regs_up<kRegsUp>();
-        bwd_group<DP, KEYS>(P, B, w, st, warp >> 2, h);
+        bwd_group<DP, KEYS, CAUSAL>(P, B, w, st, warp >> 2, h);
     } else {
         regs_down<kRegsDown>();
         if (st.n > 0) {

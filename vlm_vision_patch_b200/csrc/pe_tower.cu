@@ -572,7 +572,7 @@ pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, 
         P.part_lse2 = P.part_out + (int64_t)plan.splits * a->Hq * Nq * D;
     }
     cudaStream_t st = (cudaStream_t)stream;
-    auto run = [&](auto dp, auto groups) -> pe_status {
+    auto run = [&](auto dp, auto groups, auto causal) -> pe_status {
         constexpr int DP = decltype(dp)::value, G = decltype(groups)::value;
         using S = FwdShape<DP, G>;
         CUtensorMap mq, mk, mv;
@@ -580,7 +580,7 @@ pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, 
         mk = mv = mq;                                       // without keys their maps are not read
         if (Nk > 0 && (!make_heads_tmap(&mk, k, Nk, a->Hkv, D, S::KT) || !make_heads_tmap(&mv, v, Nk, a->Hkv, D, S::KT)))
             return PE_ERR_CUDA;
-        auto kern = pe_attn_fwd_kernel<DP, G>;
+        auto kern = pe_attn_fwd_kernel<DP, G, decltype(causal)::value>;
         static std::atomic<uint64_t> done{0};
         if (!ready_to_launch(kern, S::kSmem, a->dev, done, G == 1 ? 0 : kLaunchRegs)) return PE_ERR_CUDA;
         kern<<<grid, S::kThreads, S::kSmem, st>>>(mq, mk, mv, P);
@@ -591,7 +591,8 @@ pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, 
         return finish(cudaGetLastError());
     };
     return with_head_size(D, [&](auto dp) {
-        return plan.groups == 1 ? run(dp, std::integral_constant<int, 1>()) : run(dp, std::integral_constant<int, 2>());
+        auto of = [&](auto g) { return a->causal ? run(dp, g, std::true_type()) : run(dp, g, std::false_type()); };
+        return plan.groups == 1 ? of(std::integral_constant<int, 1>()) : of(std::integral_constant<int, 2>());
     });
 }
 
@@ -645,10 +646,11 @@ pe_status pe_attention_backward(pe_attention *a, int n_seq, const int32_t *cu_q,
     // the maps of a side without rows are not read
     if (Nq == 0) mq = mk, md = mv;
     if (Nk == 0) mk = mq, mv = md;
-    return with_head_size(D, [&](auto dp) {
+    auto run = [&](auto dp, auto causal) -> pe_status {
         constexpr int DP = decltype(dp)::value;
-        auto dq_kern = pe_attn_bwd_kernel<DP, false>;
-        auto dkv_kern = pe_attn_bwd_kernel<DP, true>;
+        constexpr bool CAUSAL = decltype(causal)::value;
+        auto dq_kern = pe_attn_bwd_kernel<DP, false, CAUSAL>;
+        auto dkv_kern = pe_attn_bwd_kernel<DP, true, CAUSAL>;
         static std::atomic<uint64_t> dq_done{0}, dkv_done{0};
         if (!ready_to_launch(dq_kern, BwdShape<DP, false>::kSmem, a->dev, dq_done) ||
             !ready_to_launch(dkv_kern, BwdShape<DP, true>::kSmem, a->dev, dkv_done))
@@ -673,7 +675,8 @@ pe_status pe_attention_backward(pe_attention *a, int n_seq, const int32_t *cu_q,
                 return finish(launch_after(pe_attn_join_grads_kernel, dim3((unsigned)((Nk * a->Hkv + 7) / 8)), 256, 0, st, P));
         }
         return finish(cudaGetLastError());
-    });
+    };
+    return with_head_size(D, [&](auto dp) { return a->causal ? run(dp, std::true_type()) : run(dp, std::false_type()); });
 }
 
 }  // extern "C"
