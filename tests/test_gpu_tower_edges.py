@@ -115,3 +115,33 @@ def test_causal_rows_do_not_see_later_rows(D, Hq, Hkv, ql, kl, at, where, value)
         assert not got["dv"][k0:k0 + last, :, 5 * c].isfinite().any()
     if math.isnan(value) and where == "q":
         assert got["out"][q0 + t].isnan().all() and got["dk"][k0:k0 + last].isnan().all()
+
+
+# ------------------------------------------------------------------ values that are not finite, seen
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,ql,causal", [(80, 2, 2, (300, 70), False), (64, 4, 2, (257,), True), (128, 2, 1, (200, 90), True),
+                                                (96, 2, 2, (130,), False)])
+def test_dv_does_not_depend_on_v(D, Hq, Hkv, ql, causal):
+    """dv_j = sum_i p_ij dout_i: a NaN in v makes out, dq and dk NaN (through delta), and
+    dv is what it was; an infinite element of dout reaches its own column of dv only."""
+    n = sum(ql)
+    q, do = normal(15, n, Hq, D, dtype=BF), normal(18, n, Hq, D, dtype=BF)
+    k, v = normal(16, n, Hkv, D, dtype=BF), normal(17, n, Hkv, D, dtype=BF)
+    att = vp.Attention(Hq, Hkv, D, causal=causal)
+    clean = run_attention(att, q, k, v, do, cu(ql), cu(ql))
+    bad = v.clone()
+    bad[3, :, 1] = math.nan
+    got = run_attention(att, q, k, bad, do, cu(ql), cu(ql))
+    assert torch.equal(got["dv"], clean["dv"]) and torch.equal(got["lse"], clean["lse"])
+    seen = slice(3 if causal else 0, ql[0])
+    assert got["out"][seen, :, 1].isnan().all() and got["dq"][seen].isnan().all()
+    assert not got["dk"][:ql[0]].isfinite().any()
+    for x in ("out", "dq", "dk"):
+        assert torch.equal(got[x][ql[0]:], clean[x][ql[0]:])
+    bad = do.clone()
+    bad[ql[0] - 1, :, 2] = math.inf                       # the row that sees every key
+    got = run_attention(att, q, k, v, bad, cu(ql), cu(ql))
+    other = [d for d in range(D) if d != 2]
+    assert torch.equal(got["dv"][..., other], clean["dv"][..., other])
+    assert (got["dv"][:ql[0], :, 2] == math.inf).all() and not got["dk"][:ql[0]].isfinite().any()

@@ -1064,7 +1064,10 @@ __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const
         if (KEYS || !mine || g != 0) return;
         // a row that sees no key has lse = -inf; with a large finite value its p is 0 and no product inf * 0
         const int64_t at = (int64_t)h * P.Nq + w.q0 + i;
-        const uint2 u = split3(limit > 0 ? -P.lse[at] / P.scale : -1e30f), v = split3(ndelta);
+        const uint2 u = split3(limit > 0 ? -P.lse[at] / P.scale : -1e30f);
+        // a delta that is not finite would reach s, and so dv, through the zeros it meets there: three times
+        // bf16's largest value is 0 there and overflows in dp
+        const uint2 v = ndelta - ndelta == 0.f ? split3(ndelta) : make_uint2(0x7F7F7F7Fu, 0x00007F7Fu);
         P.stat[at] = make_uint4(u.x, u.y, v.x, v.y);
     };
     // scores and dp of tile j, the n-th of this buffer, into registers
