@@ -31,25 +31,68 @@ __device__ __forceinline__ bool try_wait(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
+// What the roles of a block share about waiting.
+struct Waits {
+    int abort;                    // a wait has given up
+#ifdef PE_DEBUG_BOUNDS
+    long long limit;              // clock ticks after which one does
+#endif
+};
+
 // A converged warp waits for a phase of a barrier that only this block arrives on;
 // bounded like mbar_wait.  Every branch is the whole warp's, so a wait that is
 // already over costs one look and one vote (a loop that lanes could leave one by
 // one cost the issuing warps about 200 clocks per wait more).
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+#ifndef PE_DEBUG_BOUNDS
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile Waits *waits) {
     if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
     const long long t0 = clock64();
     while (!__all_sync(0xffffffffu, try_wait(bar, parity))) {
-        if (__any_sync(0xffffffffu, *abort != 0 || clock64() - t0 > kWaitClocks)) {
-            *abort = 1;
+        if (__any_sync(0xffffffffu, waits->abort != 0 || clock64() - t0 > kWaitClocks)) {
+            waits->abort = 1;
             return false;
         }
     }
     return true;
 }
-// After an abort: waits for what is in flight, by the clock alone.
+#else
+// The bounds-checking build lets tests set the limit, and looks at it before the
+// hardware's own wait, which outlasts any load (in the product library this order took
+// the backward kernels 3% longer).
+__device__ __forceinline__ bool phase_over(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile Waits *waits) {
+    if (__all_sync(0xffffffffu, phase_over(bar, parity))) return true;
+    const long long t0 = clock64();
+    do {
+        if (__any_sync(0xffffffffu, waits->abort != 0 || clock64() - t0 > waits->limit)) {
+            waits->abort = 1;
+            return false;
+        }
+    } while (!__all_sync(0xffffffffu, try_wait(bar, parity)));
+    return true;
+}
+#endif
+// A role that has begun loads or products waits for them before it ends, by the clock
+// alone and whether a wait of its own has given up or not: another role's may do so
+// later, and the block then ends without a look at what is in flight.
 __device__ __forceinline__ void warp_drain(uint64_t *bar, uint32_t parity) {
-    int never = 0;
-    warp_wait(bar, parity, &never);
+    const long long t0 = clock64();
+    while (!__all_sync(0xffffffffu, try_wait(bar, parity)))
+        if (__any_sync(0xffffffffu, clock64() - t0 > kWaitClocks)) return;
+}
+// The loads outside the ring, and the last of those begun in it.
+__device__ __forceinline__ void drain_loads(uint64_t *first, uint64_t *full, int stages, int begun) {
+    warp_drain(first, 0);
+    for (int s = max(begun - stages, 0); s < begun; ++s) warp_drain(&full[s % stages], (s / stages) & 1);
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int32_t x, int32_t y,
@@ -195,6 +238,9 @@ struct AttnParams {
                                   // keys [splits, 2, Nk, Hkv, D], dv then dk
     uint4 *stat;                  // [Hq, Nq]: -lse / scale and -dout . out, three bf16 and a 0 each (backward)
     int *err;
+#ifdef PE_DEBUG_BOUNDS
+    long long wait_clocks;        // after which a wait gives up
+#endif
 };
 
 // Boundary s of a cumulative-length array, held inside [0, n] whatever it says.
@@ -443,12 +489,12 @@ struct FwdShape {
 struct FwdBars {
     uint64_t full[8], empty[8], tail, qfull, s_full[2], s_free[2], p_full[2], pv_done[2], drain[2], turn[2][4];
     uint32_t tmem;
-    int abort;
+    Waits waits;
     Work w;
     volatile int keys[4 * 2][2];                 // per softmax warp: this block's first key and keys behind it, for the end
 };
 
-// MMAs in flight finish before their tensor memory is freed.
+// This warp's MMAs finish before their tensor memory is freed.
 __device__ __forceinline__ void drain_mmas(uint32_t one, uint64_t *bar) {
     if (one) mma_commit(bar);
     __syncwarp();
@@ -484,7 +530,7 @@ template <int DP, int G, bool CAUSAL>
 __device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, const Work &w, int tile, int n_kv, int n_other, int kb, int h) {
     using S = FwdShape<DP, G>;
     constexpr int C = S::KT / 16;
-    volatile int *abort = &B.abort;
+    volatile Waits *abort = &B.waits;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t lanes = B.tmem + ((uint32_t)(warp & 3) << 21);  // 32 lanes a warp, in bits 16..
     const uint32_t ts = lanes + S::kColS + tile * S::KT, tp = lanes + S::kColP + tile * (S::KT / 2);
@@ -542,6 +588,7 @@ __device__ __forceinline__ void fwd_softmax(const AttnParams &P, FwdBars &B, con
                     for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                     tmem_st_x16(to + 16 * c, o);
                 }
+                tmem_st_wait();                                    // (the next wait may give up)
             }
         }
         // a NaN or +inf score makes the row NaN, as the formula does; a row that has seen no key stays at 0
@@ -688,7 +735,7 @@ __device__ __forceinline__ void fwd_load(const AttnParams &P, FwdBars &B, const 
                                          int n_max, int kb, int h, int hk) {
     using S = FwdShape<DP, G>;
     constexpr int KT = S::KT;
-    volatile int *abort = &B.abort;
+    volatile Waits *abort = &B.waits;
     const int lane = threadIdx.x & 31;
     if (n_max > 0 && lane == 0) {
         const int rows = kTile / P.pack;                    // the box of mq: rows x pack heads
@@ -730,10 +777,7 @@ __device__ __forceinline__ void fwd_load(const AttnParams &P, FwdBars &B, const 
             if (lane == 0) mbar_arrive(smem_addr(&B.full[slot]));
         }
     }
-    if (!ok) {   // a wait gave up: the copies in flight still land before the block ends
-        warp_drain(&B.qfull, 0);
-        for (int s = max(f - S::kStages, 0); s < f; ++s) warp_drain(&B.full[s % S::kStages], (s / S::kStages) & 1);
-    }
+    if (n_max > 0) drain_loads(&B.qfull, B.full, S::kStages, f);
 }
 
 // MMAs of one query tile (one warp): S of the next keys as soon as the softmax has
@@ -746,7 +790,7 @@ __device__ __forceinline__ void fwd_mma(FwdBars &B, const Work &w, uint8_t *sq, 
     using S = FwdShape<DP, G>;
     constexpr int KT = S::KT;
     constexpr uint32_t kIdS = idesc_bf16_f32(kTile, KT), kIdO = idesc_b_mn(kTile, DP);
-    volatile int *abort = &B.abort;
+    volatile Waits *abort = &B.waits;
     const uint32_t one = elect_one(), tm = B.tmem;
     const uint32_t d_q = desc_k(smem_addr(sq)) + t * (S::kQ >> 4), d_k = desc_k(smem_addr(ring));
     const uint32_t d_v = desc_mn<S::kChunk>(smem_addr(ring));
@@ -809,7 +853,7 @@ __device__ __forceinline__ void fwd_mma(FwdBars &B, const Work &w, uint8_t *sq, 
         }
         r.next();
     }
-    if (!ok) drain_mmas(one, &B.drain[t]);
+    drain_mmas(one, &B.drain[t]);
 }
 
 // mk, mv: boxes of FwdShape::KT rows; mq: of 128 / pack rows and pack heads.
@@ -832,7 +876,10 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         w.z = at.z;
         if (lane == 0) {
             B.w = w;
-            B.abort = 0;
+            B.waits.abort = 0;
+#ifdef PE_DEBUG_BOUNDS
+            B.waits.limit = P.wait_clocks;
+#endif
             const int tiles = G > 1 && P.tiles > 1 && w.lq - w.row > rows ? 2 : 1;  // each gives a slot back
             for (int i = 0; i < S::kStages; ++i) mbar_init(smem_addr(&B.full[i]), 1), mbar_init(smem_addr(&B.empty[i]), tiles);
             mbar_init(smem_addr(&B.tail), 1);
@@ -887,7 +934,7 @@ pe_attn_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0 && B.abort) atomicExch(P.err, (int)PE_ERR_DEVICE_TIMEOUT);
+    if (threadIdx.x == 0 && B.waits.abort) atomicExch(P.err, (int)PE_ERR_DEVICE_TIMEOUT);
     if (warp == kLoad) {
         tc_fence_after();
         tmem_dealloc(B.tmem, S::kCols);
@@ -971,7 +1018,7 @@ struct BwdBars {
     uint64_t full[kBwdMaxStages], empty[kBwdMaxStages], tail, xfull, s_full[2], s_free[2], d_full[2], acc_done[2], acc_full, off_full, drain[3];
     float off[2][kTile];                          // what delta is off by, each group's part
     uint32_t tmem;
-    int abort;
+    Waits waits;
     Work w;
     Stream st;
 };
@@ -1035,7 +1082,7 @@ __device__ __forceinline__ void bwd_chunk(const uint32_t (&s)[16], const uint32_
 template <int DP, bool KEYS, bool CAUSAL>
 __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const Work &w, Stream st, int g, int h) {
     using T = BwdCols<DP, KEYS>;
-    volatile int *abort = &B.abort;
+    volatile Waits *abort = &B.waits;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t lanes = B.tmem + ((uint32_t)(warp & 3) << 21);
     const uint32_t ts = lanes + g * T::kBuf, tp = lanes + T::p(g), td = lanes + T::ds(g);
@@ -1248,7 +1295,7 @@ __device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const 
     using S = BwdShape<DP, KEYS>;
     constexpr int kC = kChunks<DP>;
     constexpr uint32_t kKept = S::kKept, kOne = S::kOne;                       // bytes of one kept / streamed tile
-    volatile int *abort = &B.abort;
+    volatile Waits *abort = &B.waits;
     const int lane = threadIdx.x & 31;
     const int y_len = KEYS ? w.lq : w.lk;                   // streamed rows of the sequence
     const int x_row = (KEYS ? w.k0 : w.q0) + w.row;
@@ -1304,10 +1351,7 @@ __device__ __forceinline__ void bwd_load(const AttnParams &P, BwdBars &B, const 
             if (lane == 0) mbar_arrive(smem_addr(&B.full[slot]));
         }
     }
-    if (!ok) {   // a wait gave up: the copies in flight still land before the block ends
-        warp_drain(&B.xfull, 0);
-        for (int s = max(f - S::kStages, 0); s < f; ++s) warp_drain(&B.full[s % S::kStages], (s / S::kStages) & 1);
-    }
+    drain_loads(&B.xfull, B.full, S::kStages, f);
 }
 
 // s and dp of every second streamed tile, buffer b (one warp each: while one waits
@@ -1318,7 +1362,7 @@ __device__ __forceinline__ void bwd_scores(BwdBars &B, Stream st, uint8_t *kept,
     using T = BwdCols<DP, KEYS>;
     using S = BwdShape<DP, KEYS>;
     constexpr uint32_t kKept = S::kKept, kOne = S::kOne, kIdS = idesc_bf16_f32(kTile, kStream);
-    volatile int *abort = &B.abort;
+    volatile Waits *abort = &B.waits;
     const uint32_t one = elect_one(), tm = B.tmem;
     const uint32_t x0 = desc_k(smem_addr(kept)), x1 = desc_k(smem_addr(kept + kKept));
     bool ok = warp_wait(&B.xfull, 0, abort);
@@ -1347,7 +1391,7 @@ __device__ __forceinline__ void bwd_scores(BwdBars &B, Stream st, uint8_t *kept,
         }
         __syncwarp();
     }
-    if (!ok) drain_mmas(one, &B.drain[b]);
+    drain_mmas(one, &B.drain[b]);
 }
 
 // The sums over the streamed tiles (one warp).
@@ -1356,7 +1400,7 @@ __device__ __forceinline__ void bwd_sums(BwdBars &B, Stream st, uint8_t *ring, i
     using T = BwdCols<DP, KEYS>;
     using S = BwdShape<DP, KEYS>;
     constexpr uint32_t kOne = S::kOne, kIdA = idesc_b_mn(kTile, DP);
-    volatile int *abort = &B.abort;
+    volatile Waits *abort = &B.waits;
     const uint32_t one = elect_one(), tm = B.tmem;
     // kept rows += A (tensor memory) times the streamed tile at z
     auto add = [&](uint32_t acc, uint32_t a, uint32_t z, int steps, bool more) {
@@ -1392,7 +1436,7 @@ __device__ __forceinline__ void bwd_sums(BwdBars &B, Stream st, uint8_t *ring, i
         }
         __syncwarp();
     }
-    if (!ok) drain_mmas(one, &B.drain[2]);
+    drain_mmas(one, &B.drain[2]);
 }
 
 // mx0, mx1: maps of the kept tensors, my0, my1 of the streamed ones (boxes of 64 rows).
@@ -1415,7 +1459,10 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
         if (lane == 0) {
             B.w = w;
             if (w.row >= 0) B.st = stream_of<KEYS>(P, w, w.h);
-            B.abort = 0;
+            B.waits.abort = 0;
+#ifdef PE_DEBUG_BOUNDS
+            B.waits.limit = P.wait_clocks;
+#endif
             for (int i = 0; i < S::kStages; ++i) {
                 mbar_init(smem_addr(&B.full[i]), 1);
                 mbar_init(smem_addr(&B.empty[i]), 1);
@@ -1481,7 +1528,7 @@ pe_attn_bwd_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constan
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0 && B.abort) atomicExch(P.err, (int)PE_ERR_DEVICE_TIMEOUT);
+    if (threadIdx.x == 0 && B.waits.abort) atomicExch(P.err, (int)PE_ERR_DEVICE_TIMEOUT);
     if (warp == 8) {
         tc_fence_after();
         tmem_dealloc(B.tmem, 512);

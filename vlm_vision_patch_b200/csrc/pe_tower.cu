@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 #include <new>
 #include <type_traits>
@@ -531,6 +532,10 @@ static AttnParams attention_params(const pe_attention *a, int n_seq, const int32
     P.causal = a->causal;
     P.scale = a->scale;
     P.err = a->err;
+#ifdef PE_DEBUG_BOUNDS
+    const char *ns = std::getenv("PE_TEST_WAIT_NS");      // two clock ticks each
+    P.wait_clocks = ns ? 2 * std::atoll(ns) : kWaitClocks;
+#endif
     return P;
 }
 
