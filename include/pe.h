@@ -635,7 +635,7 @@ int64_t pe_attention_workspace(const pe_attention *a, int n_seq, int64_t Nq, int
  * elements and at least D (pe_heads), and smaller than 2^39 elements; the heads
  * of out must not overlap.  A row that sees no key gets out = 0 and lse = -inf;
  * one that sees keys, all with scores of -inf, out = NaN and lse = -inf.  Rows
- * of no sequence are left as they were.  n_seq = 0 or Nq = 0: nothing is launched.
+ * of no sequence are left as they were.  out must not overlap q, k or v.  n_seq = 0 or Nq = 0: nothing is launched.
  * Errors: PE_ERR_INVALID_ARG, PE_ERR_SHAPE, PE_ERR_ALIGN, PE_ERR_UNSUPPORTED
  * (Nq or Nk >= 2^31), PE_ERR_CUDA.
  */

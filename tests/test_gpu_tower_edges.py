@@ -145,3 +145,36 @@ def test_dv_does_not_depend_on_v(D, Hq, Hkv, ql, causal):
     other = [d for d in range(D) if d != 2]
     assert torch.equal(got["dv"][..., other], clean["dv"][..., other])
     assert (got["dv"][:ql[0], :, 2] == math.inf).all() and not got["dk"][:ql[0]].isfinite().any()
+
+
+# ------------------------------------------------------------------ rows of no sequence
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,causal,pre,ql,kl,post", [
+    (80, 2, 2, False, 0, (130, 61), None, 200),
+    (64, 2, 1, True, 7, (300, 0, 45), None, 19),
+    (128, 12, 2, True, 3, (1, 1), (5000, 3000), 2),           # divided keys, packed heads
+    (72, 20, 20, False, 0, (64,) * 12, None, 700),            # blocks of one tile
+    (96, 2, 2, False, 5, (0, 0), None, 4),                    # every sequence empty
+    (96, 2, 2, False, 5, (), None, 4),                        # no sequence
+    (128, 12, 2, True, 100, (200,), (300,), 3000),            # dk and dv in parts
+])
+def test_padded_batches_in_tensors_that_hold_zeros(D, Hq, Hkv, causal, pre, ql, kl, post):
+    """Rows before the first and behind the last sequence keep what given tensors held,
+    in every form of the kernels, whatever the inputs hold there."""
+    kl = ql if kl is None else kl
+    nq, nk = pre + sum(ql) + post, pre + sum(kl) + post
+    q, do = normal(30, nq, Hq, D, dtype=BF), normal(33, nq, Hq, D, dtype=BF)
+    k, v = normal(31, nk, Hkv, D, dtype=BF), normal(32, nk, Hkv, D, dtype=BF)
+    mq, mk = slice(pre, pre + sum(ql)), slice(pre, pre + sum(kl))
+    R, A = attention_ref(q[mq], k[mk], v[mk], ql, kl, causal, D ** -0.5, do[mq])
+    for t, m in ((q, mq), (do, mq), (k, mk), (v, mk)):
+        t[:m.start], t[m.stop:] = math.nan, math.inf
+    att = vp.Attention(Hq, Hkv, D, causal=causal)
+    cq, ck = cu(ql) + pre, cu(kl) + pre
+    out, lse = att.forward(q, k, v, cq, ck, out=torch.zeros_like(q))
+    dq, dk, dv = att.backward(do, q, k, v, out, lse, cq, ck, dq=torch.zeros_like(q), dk=torch.zeros_like(k),
+                              dv=torch.zeros_like(v))
+    for t, n, m in ((out, "out", mq), (dq, "dq", mq), (dk, "dk", mk), (dv, "dv", mk)):
+        assert not t[:m.start].any() and not t[m.stop:].any(), n
+        close(t[m], R[n], A[n] + U[BF] * R[n].abs() + 1e-30, n)

@@ -289,7 +289,11 @@ class Attention:
         """q [Nq, heads, D], k and v [Nk, kv_heads, D] bf16 (any row and head
         strides that are multiples of 8), cu_q and cu_k int32 [n_seq + 1] on the
         device (cu_k None: cu_q).  Returns (out [Nq, heads, D] bf16, lse [heads,
-        Nq] fp32 or None).  Rows of no sequence are not written."""
+        Nq] fp32 or None).  ``out`` must not overlap q, k or v.
+
+        Rows of no sequence (padding before cu_q[0] and behind cu_q[-1]) are not
+        written: in a new ``out`` they hold whatever the memory held, NaN perhaps.
+        Where a later product reads them, give an ``out`` that holds zeros there."""
         d = self.dev
         n, cq, ck = self._cu(cu_q, cu_k)
         if _elsewhere(d, stream):
@@ -313,7 +317,12 @@ class Attention:
                  dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
                  dv: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
         """(dq, dk, dv) for the gradient dout of out; out and lse are forward's.
-        dq, dk and dv may be given (slices of one packed gradient, for instance)."""
+        dq, dk and dv may be given (slices of one packed gradient, for instance);
+        none may overlap another tensor of the call.
+
+        Rows of no sequence are not written, as in `forward`: a product over the
+        rows of a new gradient (a weight's, for instance) would add what the memory
+        held there.  For padded batches give gradients that hold zeros there."""
         d = self.dev
         n, cq, ck = self._cu(cu_q, cu_k)
         if _elsewhere(d, stream):
