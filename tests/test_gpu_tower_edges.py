@@ -238,3 +238,67 @@ def test_attention_gradients_from_flat_to_one_hot(D, std):
         # rows share their weight, on the rows with two close scores where they are one-hot
         told = (R[name].abs() > A[name]).double()
         assert told.mean() > 0.1 if std < 16 else told.sum() >= 100, name
+
+
+# ------------------------------------------------------------------ buffers with guards
+
+
+class Guards:
+    """Tensors inside larger allocations whose other elements must not change."""
+
+    def __init__(self):
+        self.all = []
+
+    def __call__(self, *shape, dtype=BF):
+        n, pad = math.prod(shape), 4096
+        flat = torch.full((n + 2 * pad,), 77.0, dtype=dtype, device=DEV)
+        self.all.append((flat, n, pad))
+        return flat[pad:pad + n].view(shape)
+
+    def check(self):
+        torch.cuda.synchronize()
+        for flat, n, pad in self.all:
+            assert (flat[:pad] == 77).all() and (flat[pad + n:] == 77).all()
+
+
+def heads(t):
+    return B.pe_heads(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,causal,nq,nk,cq,ck", [
+    (64, 1, 1, False, 300, 300, (-5, 100, 60, 5000), None),
+    (80, 4, 2, True, 300, 300, (-5, 100, 60, 5000), None),
+    (72, 2, 2, False, 131, 200, (0, 50, 131), (-2 ** 31, 2 ** 31 - 1, 3)),
+    (128, 12, 2, True, 4, 9000, (0, 1, 9, 2), (0, 9001, 4000, 20000)),     # packed and divided
+    (64, 8, 8, False, 2, 6000, (-1, 1, 7), (0, 6500, 100)),
+    (96, 24, 24, True, 500, 500, (3, 70, 130, 190, 250, 64, 330, 400, 999), None),
+    (128, 4, 2, True, 513, 700, (0, 513), (0, 700)),                       # in order, for comparison
+    (40, 2, 2, False, 77, 77, (77, 0), (0, 77)),
+])
+def test_nothing_outside_the_buffers_is_written(D, Hq, Hkv, causal, nq, nk, cq, ck):
+    """Outputs, gradients, lse and both workspaces between guards, boundaries in and out
+    of their contract."""
+    G = Guards()
+    c1 = torch.tensor(cq, dtype=torch.int32, device=DEV)
+    c2 = c1 if ck is None else torch.tensor(ck, dtype=torch.int32, device=DEV)
+    n = len(cq) - 1
+    q, do = normal(40, nq, Hq, D, dtype=BF), normal(43, nq, Hq, D, dtype=BF)
+    k, v = normal(41, nk, Hkv, D, dtype=BF), normal(42, nk, Hkv, D, dtype=BF)
+    out, dq, dk, dv = G(nq, Hq, D), G(nq, Hq, D), G(nk, Hkv, D), G(nk, Hkv, D)
+    lse = G(Hq, nq, dtype=F32)
+    att = vp.Attention(Hq, Hkv, D, causal=causal)
+    ws = [G(max(B.pe_attention_workspace(att.h, n, nq, nk, b), 16) // 4, dtype=F32) for b in (False, True)]
+    st = torch.cuda.current_stream().cuda_stream
+    B.pe_attention_forward(att.h, n, c1.data_ptr(), nq, c2.data_ptr(), nk, heads(q), heads(k), heads(v), heads(out),
+                           lse.data_ptr(), ws[0].data_ptr(), ws[0].numel() * 4, st)
+    B.pe_attention_backward(att.h, n, c1.data_ptr(), nq, c2.data_ptr(), nk, heads(q), heads(k), heads(v), heads(out),
+                            lse.data_ptr(), heads(do), heads(dq), heads(dk), heads(dv), ws[1].data_ptr(), ws[1].numel() * 4, st)
+    G.check()
+    if cq[0] == -5:                                        # rows 0 .. 59 belong to the first sequence, of 100 rows, alone
+        R, A = attention_ref(q[:100], k[:100], v[:100], (100,), (100,), causal, D ** -0.5, do[:100])
+        for got, x in ((out, "out"), (dq, "dq")):
+            close(got[:60], R[x][:60], A[x][:60] + U[BF] * R[x][:60].abs() + 1e-30, x)
+    # the same through the wrapper, whose tensors are its own
+    att.forward(q, k, v, c1, c2)
+    att.backward(do, q, k, v, out, lse, c1, c2)
+    G.check()
