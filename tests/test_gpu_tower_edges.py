@@ -302,3 +302,39 @@ def test_nothing_outside_the_buffers_is_written(D, Hq, Hkv, causal, nq, nk, cq, 
     att.forward(q, k, v, c1, c2)
     att.backward(do, q, k, v, out, lse, c1, c2)
     G.check()
+
+
+# ------------------------------------------------------------------ layer norm
+
+
+@pytest.mark.parametrize("N,E,dtype", [
+    # threads a row, chunks a thread: 32 x 5, 64 x 3, 64 x 4, 128 x 4, 256 x 4, 256 x 5, 512 x 4
+    (8003, 1280, BF), (3001, 1288, BF), (3001, 2048, BF), (2005, 4096, BF), (1301, 8192, BF), (701, 10240, BF), (701, 16384, BF),
+    (8003, 640, F32), (3001, 1152, F32), (3001, 1280, F32), (2005, 2560, F32), (1301, 4096, F32), (701, 5120, F32),
+    (701, 8192, F32), (701, 16384, F32),                      # the last keeps one row in flight
+])
+def test_layer_norm_backward_over_many_rows(N, E, dtype):
+    """More rows than the resident blocks hold at once (three to five times, the last
+    group partly empty): ring slots, row sums and weight sums are used again and again."""
+    x = normal(50, N, E, dtype=dtype, std=1.5, mean=-0.2)
+    g = normal(51, E, dtype=dtype, std=0.2, mean=1.0)
+    dy = normal(52, N, E, dtype=dtype)
+    _, mean, rstd = vp.layer_norm(x, g, None, 1e-5, stats=True)
+    dx, dg, db = vp.layer_norm_backward(dy, x, g, mean, rstd)
+    _, _, rr, z = norm_ref(x, g, None, 1e-5)
+    d, a = dy.double(), dy.double() * g.double()
+    rdx = rr[:, None] * (a - a.mean(-1, keepdim=True) - z * (a * z).mean(-1, keepdim=True))
+    tz = norm_tol(x, None, None, 0 * z, x.double().mean(-1), rr, z, F32)
+    t = (a.abs() * 4 * 2.0 ** -24 + SUM * a.abs().mean(-1, keepdim=True)
+         + tz * (a * z).mean(-1, keepdim=True).abs()
+         + z.abs() * (SUM * (a * z).abs().mean(-1, keepdim=True) + (a.abs() * tz).mean(-1, keepdim=True)))
+    close(dx, rdx, rr[:, None] * t + 2 * SUM * rdx.abs() + U[dtype] * rdx.abs(), "dx")
+    # a column's chain: the rows of one block, its other rows, the 32 x 4 sums over blocks and their join
+    chain = (64 + N / 148) * 2.0 ** -24
+    rdg, rdb = (d * z).sum(0), d.sum(0)
+    close(dg, rdg, (d.abs() * tz).sum(0) + chain * (d * z).abs().sum(0) + U[dtype] * rdg.abs(), "dgamma")
+    close(db, rdb, chain * d.abs().sum(0) + U[dtype] * rdb.abs(), "dbeta")
+    again = vp.layer_norm_backward(dy, x, g, mean, rstd)
+    assert all(torch.equal(p, w) for p, w in zip(again, (dx, dg, db)))
+    xi = x.clone()
+    assert torch.equal(vp.layer_norm_backward(dy, xi, g, mean, rstd, weight_grads=False, out=xi)[0], dx)
