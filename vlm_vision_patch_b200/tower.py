@@ -6,14 +6,21 @@ gradients (``pe_vision_positions``, ``pe_rope``, ``pe_layernorm_*`` and
 The functions run on the tensors' own device, on ``stream`` (a torch stream or
 a raw handle) or, without one, on that device's current stream.  Outputs and
 workspaces are allocated on the stream the call runs on, so calls on several
-streams share nothing and a call can be captured into a CUDA graph.  Nothing
-here records an autograd graph: the gradient calls are functions of their own.
+streams share nothing and a call can be captured into a CUDA graph.
+
+`rope`, `layer_norm` and `Attention.forward` are differentiable: with grad mode
+on and an input that requires grad they are recorded, and torch's backward pass
+makes the gradient calls below, which can also be made by hand (they are not
+recorded themselves).  A call that is recorded takes no output tensor.  Writes
+to output tensors count as in-place changes for autograd's checks.
 """
 from __future__ import annotations
 
 from typing import Optional, Sequence, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from . import _binding as B
 from . import _dt, _need, _raw_stream
@@ -23,6 +30,13 @@ __all__ = ["vision_positions", "rope", "layer_norm", "layer_norm_backward", "Att
 _I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
 _NONE = B.pe_heads(None, 0, 0)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_grad_on = torch.is_grad_enabled
+
+
+def _no_outputs(*outs: Optional[torch.Tensor]) -> None:
+    if any(t is not None for t in outs):
+        raise ValueError("a call that autograd records takes no output tensors: an input (or output) requires grad; "
+                         "leave them out, or call under torch.no_grad()")
 
 
 def _elsewhere(device: int, stream) -> bool:
@@ -130,6 +144,10 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, sections
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return rope(q, k, pos, sections, theta, axial, inverse, out_q, out_k)
+    if _grad_on() and (q.requires_grad or (k is not None and k.requires_grad)
+                       or (out_q is not None and out_q.requires_grad) or (out_k is not None and out_k.requires_grad)):
+        _no_outputs(out_q, out_k)
+        return _Rope.apply(q, k, pos, tuple(sections), theta, axial, inverse)
     if q.dim() != 3 or (k is not None and k.dim() != 3):
         raise ValueError("q and k must be [N, heads, D]")
     if pos.dim() != 2 or pos.shape[0] != len(sections):
@@ -144,6 +162,7 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, sections
         qo = B.pe_heads(out_q.data_ptr(), hq * d, d)
     else:
         qo = _heads(out_q, "out_q", dev, dtype, shape)
+        increment_version(out_q)
     hk, ks, ko = 0, _NONE, _NONE
     if k is not None:
         hk = k.shape[1]
@@ -154,8 +173,25 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, sections
             ko = B.pe_heads(out_k.data_ptr(), hk * d, d)
         else:
             ko = _heads(out_k, "out_k", dev, dtype, k_shape)
+            increment_version(out_k)
     B.pe_rope(qs, ks, dt, n, hq, hk, d, pos_ptr, sections, theta, axial, inverse, qo, ko, _raw(dev))
     return out_q, out_k if k is not None else None
+
+
+class _Rope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, pos, sections, theta, axial, inverse):
+        ctx.save_for_backward(pos)
+        ctx.how, ctx.with_k = (sections, theta, axial, not inverse), k is not None
+        return rope(q, k, pos, sections, theta, axial, inverse)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk):
+        pos, = ctx.saved_tensors
+        dq, dk = (g if g is None or g.stride(-1) == 1 else g.contiguous() for g in (dq, dk))
+        dq, dk = rope(dq, dk if ctx.with_k else None, pos, *ctx.how)
+        return dq, dk, None, None, None, None, None
 
 
 def _weights(dev: int, E: int, gamma, beta=None) -> Tuple[Optional[int], Optional[int], int]:
@@ -178,6 +214,11 @@ def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Opti
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return layer_norm(x, gamma, beta, eps, out, stats)
+    if _grad_on() and (x.requires_grad or (gamma is not None and gamma.requires_grad)
+                       or (beta is not None and beta.requires_grad) or (out is not None and out.requires_grad)):
+        _no_outputs(out)
+        y, mean, rstd = _LayerNorm.apply(x, gamma, beta, eps)
+        return (y, mean, rstd) if stats else y
     if x.dim() < 1:
         raise ValueError("x must be [..., E]")
     shape = x.shape
@@ -190,6 +231,7 @@ def layer_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Opti
         op = out.data_ptr()
     else:
         op = _dense(out, "out", dev, shape, dtype)
+        increment_version(out)
     mean = rstd = mp = rp = None
     if stats:
         mean, rstd = x.new_empty(lead, dtype=_F32), x.new_empty(lead, dtype=_F32)
@@ -226,6 +268,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch
         op = out.data_ptr()
     else:
         op = _dense(out, "out", dev, shape, x.dtype)
+        increment_version(out)
     dgamma = dbeta = gp = bp = ws = None
     nbytes = 0
     if weight_grads:
@@ -236,6 +279,25 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch
         gp, bp, ws = dgamma.data_ptr(), dbeta.data_ptr(), scratch.data_ptr()
     B.pe_layernorm_backward(dp, xp, dt, n, E, g, w_dt, mp, rp, op, gp, bp, ws, max(nbytes, 0), _raw(dev))
     return out, dgamma, dbeta
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gamma, beta, eps):
+        y, mean, rstd = layer_norm(x, gamma, beta, eps, stats=True)
+        ctx.mark_non_differentiable(mean, rstd)
+        ctx.save_for_backward(x, gamma, mean, rstd)
+        ctx.weight_dtype = None if beta is None else beta.dtype
+        return y, mean, rstd
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dmean, drstd):
+        x, gamma, mean, rstd = ctx.saved_tensors
+        need_x, need_gamma, need_beta, _ = ctx.needs_input_grad
+        dx, dgamma, dbeta = layer_norm_backward(dy.contiguous(), x, gamma, mean, rstd, need_gamma or need_beta,
+                                                weight_dtype=ctx.weight_dtype)
+        return dx if need_x else None, dgamma if need_gamma else None, dbeta if need_beta else None, None
 
 
 class Attention:
@@ -293,12 +355,17 @@ class Attention:
 
         Rows of no sequence (padding before cu_q[0] and behind cu_q[-1]) are not
         written: in a new ``out`` they hold whatever the memory held, NaN perhaps.
-        Where a later product reads them, give an ``out`` that holds zeros there."""
+        Where a later product reads them, give an ``out`` that holds zeros there.
+        (A recorded call and its gradients hold zeros.)"""
         d = self.dev
         n, cq, ck = self._cu(cu_q, cu_k)
         if _elsewhere(d, stream):
             with _on(d, stream):
                 return self.forward(q, k, v, cu_q, cu_k, out, lse)
+        if _grad_on() and (q.requires_grad or k.requires_grad or v.requires_grad or (out is not None and out.requires_grad)):
+            _no_outputs(out)
+            out, stat = _Attend.apply(self, q, k, v, cu_q, cu_k)
+            return out, stat if lse else None
         sq, sk = self._shapes(q, k)
         qs, ks, vs = _heads(q, "q", d, _BF16, sq), _heads(k, "k", d, _BF16, sk), _heads(v, "v", d, _BF16, sk)
         if out is None:
@@ -306,6 +373,7 @@ class Attention:
             os = self._fresh(out, sq)
         else:
             os = _heads(out, "out", d, _BF16, sq)
+            increment_version(out)
         stat = q.new_empty((self.heads, sq[0]), dtype=_F32) if lse else None
         ws, wp, nbytes = self._workspace(q, n, sq[0], sk[0], False)
         B.pe_attention_forward(self.h, n, cq, sq[0], ck, sk[0], qs, ks, vs, os,
@@ -339,6 +407,7 @@ class Attention:
                 grads.append((t, self._fresh(t, s)))
             else:
                 grads.append((t, _heads(t, name, d, _BF16, s)))
+                increment_version(t)
         ws, wp, nbytes = self._workspace(q, n, sq[0], sk[0], True)
         B.pe_attention_backward(self.h, n, cq, sq[0], ck, sk[0], args[0], args[1], args[2], args[3], lp, args[4],
                                 grads[0][1], grads[1][1], grads[2][1], wp, nbytes, _raw(d))
@@ -357,3 +426,21 @@ class Attention:
             self.close()
         except Exception:
             pass
+
+
+class _Attend(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, attention, q, k, v, cu_q, cu_k):
+        # rows of no sequence: zeros, here and in the gradients, as what is before and behind reads every row
+        out, lse = attention.forward(q, k, v, cu_q, cu_k, q.new_zeros(q.shape))
+        ctx.mark_non_differentiable(lse)
+        ctx.save_for_backward(q, k, v, out, lse, cu_q, cu_k)
+        ctx.attention = attention
+        return out, lse
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout, dlse):
+        q, k, v, out, lse, cu_q, cu_k = ctx.saved_tensors
+        grads = (t.new_zeros(t.shape) for t in (q, k, v))
+        return (None, *ctx.attention.backward(dout.contiguous(), q, k, v, out, lse, cu_q, cu_k, *grads), None, None)
