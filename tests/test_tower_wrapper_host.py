@@ -17,3 +17,9 @@ def test_recorded_calls_take_no_output_tensors():
             call()
         with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_positions_are_not_put_on_the_host():
+    for device in ("cpu", torch.device("cpu"), "meta"):
+        with pytest.raises(ValueError, match="CUDA device"):
+            vp.vision_positions([(1, 2, 2)], 2, device=device)

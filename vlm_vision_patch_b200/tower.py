@@ -115,7 +115,12 @@ def vision_positions(grid_thw: Sequence[Sequence[int]], merge: int = 2, device=N
         frames += t
     if n >= 2 ** 31:
         raise ValueError("the grids hold 2^31 patches or more")
-    dev = None if device is None else torch.device(device).index
+    dev = None
+    if device is not None:
+        device = torch.device(device)
+        if device.type != "cuda":
+            raise ValueError(f"device must be a CUDA device; got {device}")
+        dev = device.index
     if dev is None:
         dev = _current_device()
     if _elsewhere(dev, stream):
