@@ -544,7 +544,8 @@ pe_status pe_vision_positions(int n, const int32_t *grid_thw, int merge, int32_t
  * rounded once.  Pointers need only the alignment of dt.
  * The heads of an output must not overlap.
  * Requires 1 <= D <= 1024, 1 <= S <= PE_ROPE_MAX_PAIRS, 2 S <= D, 1 <= axes <=
- * PE_ROPE_MAX_AXES, theta > 0 and finite, N < 2^31, Hq >= 1, strides >= 0.
+ * PE_ROPE_MAX_AXES, theta > 0 and finite with rates of at most 2^990, N < 2^31,
+ * Hq >= 1, strides >= 0.
  * Errors: PE_ERR_INVALID_ARG, PE_ERR_SHAPE, PE_ERR_DTYPE, PE_ERR_ALIGN,
  * PE_ERR_UNSUPPORTED, PE_ERR_CUDA.
  */
@@ -650,8 +651,10 @@ pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, 
  *     dv_j = sum_i p_ij dout_i,  ds_ij = p_ij (dout_i . v_j - delta_i),
  *     dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,
  * the sums for dk and dv over the query heads that share the key head as well.
+ * lse is stored in fp32, so p is off by a factor of up to exp(2^-22 |s|): scores
+ * beyond some 10^5 (a scale far from D^-1/2) leave few digits of the gradient.
  *   dq : [Nq, Hq, D] bf16;  dk, dv : [Nk, Hkv, D] bf16, layouts as out's.  None
- *   may overlap an input.  Rows that see no key, and keys that no row sees, get
+ *   may overlap an input or another of them.  Rows that see no key, and keys that no row sees, get
  *   zero gradients; rows of no sequence are left as they were.
  * Other arguments and errors as pe_attention_forward (lse not NULL).
  */

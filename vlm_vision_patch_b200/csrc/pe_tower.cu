@@ -347,6 +347,12 @@ pe_status pe_rope(pe_heads q, pe_heads k, pe_dtype dt, int64_t N, int Hq, int Hk
     }
     if (S < 1 || 2 * S > D) return PE_ERR_SHAPE;
     if (S > PE_ROPE_MAX_PAIRS || (int64_t)Hq + Hk > 65536) return PE_ERR_UNSUPPORTED;
+    // a position (below 2^31) times the largest rate is finite
+    const double log2_theta = std::log2(theta);
+    for (int a = 0; a < axes; ++a) {
+        const double n = axial ? (double)sections[a] : (double)S;
+        if (n > 0 && -(n - 1) / n * log2_theta > 990) return PE_ERR_UNSUPPORTED;
+    }
     if (N == 0) return PE_OK;
     if (!pos) return PE_ERR_INVALID_ARG;
     if (!aligned_to(pos, 4)) return PE_ERR_ALIGN;
@@ -370,7 +376,7 @@ pe_status pe_rope(pe_heads q, pe_heads k, pe_dtype dt, int64_t N, int Hq, int Hk
     P.pairs = (int)S;
     P.tail = (int)(D - 2 * S);
     P.sign = inverse ? -1.f : 1.f;
-    const double two_pi = 6.283185307179586476925286766559, log2_theta = std::log2(theta);
+    const double two_pi = 6.283185307179586476925286766559;
     for (int a = 0, i = 0; a < axes; ++a)
         for (int j = 0; j < sections[a]; ++j, ++i) {
             P.axis[i] = (uint8_t)a;
