@@ -654,8 +654,9 @@ pe_status pe_attention_forward(pe_attention *a, int n_seq, const int32_t *cu_q, 
  * lse is stored in fp32, so p is off by a factor of up to exp(2^-22 |s|): scores
  * beyond some 10^5 (a scale far from D^-1/2) leave few digits of the gradient.
  *   dq : [Nq, Hq, D] bf16;  dk, dv : [Nk, Hkv, D] bf16, layouts as out's.  None
- *   may overlap an input or another of them.  Rows that see no key, and keys that no row sees, get
- *   zero gradients; rows of no sequence are left as they were.
+ *   may overlap an input or another of them.  Rows that see no key, and keys
+ *   that no row sees, get zero gradients; rows of no sequence are left as they
+ *   were.
  * Other arguments and errors as pe_attention_forward (lse not NULL).
  */
 pe_status pe_attention_backward(pe_attention *a, int n_seq, const int32_t *cu_q, int64_t Nq, const int32_t *cu_k,

@@ -1,7 +1,9 @@
 // Row-wise kernels of the vision tower: patch positions from grids, rotary
 // positions, and layer norm with its gradient.  All are bound by HBM (or, on one
-// image, by launch latency): each reads its rows once with 16-byte loads, keeps
-// them in registers and writes once.
+// image, by launch latency): each reads its rows once, with 16-byte accesses where
+// sizes and strides allow (rotary positions take narrower ones elsewhere), and writes
+// once.  Rows stay in registers in between, those of the layer norm's gradient in
+// shared memory.
 #pragma once
 
 #include <cstdint>
