@@ -12,7 +12,9 @@ streams share nothing and a call can be captured into a CUDA graph.
 on and an input that requires grad they are recorded, and torch's backward pass
 makes the gradient calls below, which can also be made by hand (they are not
 recorded themselves).  A call that is recorded takes no output tensor.  Writes
-to output tensors count as in-place changes for autograd's checks.
+to output tensors count as in-place changes for autograd's checks.  As with
+torch's own operators, a backward pass can be captured while no eager graph of
+its leaves lives.
 """
 from __future__ import annotations
 
