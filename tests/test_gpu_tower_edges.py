@@ -117,6 +117,22 @@ def test_causal_rows_do_not_see_later_rows(D, Hq, Hkv, ql, kl, at, where, value)
         assert got["out"][q0 + t].isnan().all() and got["dk"][k0:k0 + last].isnan().all()
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,ql,kl", [(96, 1, 1, (200,), (130,)), (8, 2, 1, (1, 18), (1, 5)), (128, 6, 1, (30, 392), (30, 277))])
+def test_causal_rows_without_keys_stay_zero(D, Hq, Hkv, ql, kl):
+    """Early rows of a sequence with fewer keys see none: 0 out and 0 gradient, whatever the
+    keys of their tile hold."""
+    nq, nk = sum(ql), sum(kl)
+    q, do = normal(14, nq, Hq, D, dtype=BF), normal(19, nq, Hq, D, dtype=BF)
+    k, v = normal(24, nk, Hkv, D, dtype=BF), normal(25, nk, Hkv, D, dtype=BF)
+    lo, free = nq - ql[-1], ql[-1] - kl[-1]
+    first = nk - kl[-1]
+    k[first + 2:], v[first + 2:] = math.nan, math.inf
+    got = run_attention(vp.Attention(Hq, Hkv, D, causal=True), q, k, v, do, cu(ql), cu(kl))
+    none = slice(lo, lo + free)
+    assert not got["out"][none].any() and not got["dq"][none].any() and torch.isneginf(got["lse"][:, none]).all()
+    assert got["dq"][none.stop:none.stop + 2].isfinite().all() and got["dq"][none.stop + 2:].isnan().all()
+
+
 # ------------------------------------------------------------------ values that are not finite, seen
 
 

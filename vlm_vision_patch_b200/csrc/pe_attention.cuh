@@ -1243,7 +1243,7 @@ __device__ __forceinline__ void bwd_group(const AttnParams &P, BwdBars &B, const
     // Streamed rows that the mask hides from a kept one: keys from `limit` on (fewer for every
     // later query), queries before i - shift (more for every later key).
     const int hidden = KEYS ? i - shift : limit, edge = KEYS ? st.first * kStream : min(st.n * kStream, w.lk);
-    const bool whole = KEYS || (nlse2 - nlse2 == 0.f && ndelta - ndelta == 0.f);
+    const bool whole = KEYS || limit == 0 || (nlse2 - nlse2 == 0.f && ndelta - ndelta == 0.f);   // (no key seen: 0)
     const bool some = mine && whole && (KEYS ? edge < hidden : hidden < edge);
     if (!__any_sync(0xffffffffu, some)) return;
     const bool lost = KEYS ? tmem_odd<DP / 16>(acc, 16) : tmem_odd<(DP / 16 + 1) / 2>(acc + 16 * g, 32, DP / 16 - g);
